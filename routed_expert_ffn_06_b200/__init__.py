@@ -6,4 +6,4 @@ C ABI in ``include/moe.h`` and is reached through :mod:`.moe` (ctypes binding);
 the seeded synthetic inputs come from :mod:`.synth`.
 """
 
-__all__ = ["moe", "synth"]
+__all__ = ["moe", "moe_ops", "synth"]

@@ -18,17 +18,19 @@ NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", 
 
 
 HOST = os.path.join(PKG, "host")   # host-only code (the weight packer)
+OPS = os.path.join(PKG, "ops")     # the operators of include/moe_ops.h
 
 
 def sources():
-    return sorted(glob.glob(os.path.join(CSRC, "*.cu"))) + sorted(glob.glob(os.path.join(HOST, "*.cu")))
+    return [p for d in (CSRC, HOST, OPS) for p in sorted(glob.glob(os.path.join(d, "*.cu")))]
 
 
 def stale() -> bool:
     if not os.path.exists(LIB):
         return True
     t = os.path.getmtime(LIB)
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
+    deps = sources() + [p for d in (CSRC, OPS) for x in ("*.cuh", "*.h")
+                        for p in glob.glob(os.path.join(d, x))]
     deps += glob.glob(os.path.join(INCLUDE, "*.h"))
     return any(os.path.getmtime(p) > t for p in deps)
 

@@ -1,0 +1,256 @@
+// norm.cu -- the norms before and after a block, fused with the block's gate
+// and the residual scales, and the quantiser of bf16 rows to e4m3.
+//
+//   u = y [* rsqrt(mean(y^2) + eps) * W(post_w)]
+//   r = a x + b act(gate) u              -> x_out
+//   h = r * rsqrt(mean(r^2) + eps) * W(pre_w)   -> bf16 and/or e4m3 with a
+//                                           scale per 128 columns
+//
+// One pass over memory: a row stays in registers between the loads and the
+// stores, so every byte is read once and written once; the kernel is bound by
+// HBM for many rows and by its launch and two dependent reductions for one.
+// A thread owns chunks of 8 consecutive channels (16-byte accesses in bf16).
+// Rows of up to 1024 channels take one warp each (no block barrier); wider
+// rows take a block each.  128 channels are 16 chunks = 16 consecutive lanes,
+// so the largest |h| of a scale block is a half-warp maximum.
+#include "ops.h"
+
+namespace moe {
+
+namespace {
+
+__device__ __forceinline__ void unpack8(const uint4& v, float (&o)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    o[2 * j] = __uint_as_float(w[j] << 16);
+    o[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+  }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+    w[j] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ void load8f(const float* p, float (&o)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w, o[4] = b.x, o[5] = b.y, o[6] = b.z, o[7] = b.w;
+}
+
+// Four floats to four e4m3 codes, nearest with ties to even, clamped to +-448.
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+  return (uint32_t)lo | ((uint32_t)hi << 16);
+}
+
+// Quantise one chunk of 8 channels of a block of 16 lanes.  The maximum is
+// taken over the bit patterns of |v|, so that a NaN or infinity survives it.
+// `live`: the chunk lies inside the row (all lanes of the warp call this).
+__device__ __forceinline__ void quant8(const float (&v)[8], bool live, uint8_t* codes,
+                                       float* scale) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+  if (!live) m = 0;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float s = __fdiv_rn(__uint_as_float(m), kE4m3Max);
+  if (!live) return;
+  float q[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) q[j] = s != 0.f ? __fdiv_rn(v[j], s) : v[j];
+  *reinterpret_cast<uint2*>(codes) =
+      make_uint2(e4m3x4(q[0], q[1], q[2], q[3]), e4m3x4(q[4], q[5], q[6], q[7]));
+  if ((threadIdx.x & 15) == 0) *scale = s;
+}
+
+// Sum over the row's threads: a warp, or the whole block (red: a float per
+// warp; one barrier, so two sums of one row use two arrays).
+template <bool WARP_ROW>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+  v = warp_sum(v);
+  if (WARP_ROW) return v;
+  const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+  if (lane == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  return warp_sum(lane < nw ? red[lane] : 0.f);
+}
+
+constexpr int kWarpRows = 4;   // rows (warps) of a block when a row takes one warp
+
+template <bool F32, bool WARP_ROW, int CH>
+__global__ void __launch_bounds__(WARP_ROW ? 32 * kWarpRows : 1024) norm_block_kernel(NormArgs a) {
+  __shared__ float red[2][32];
+  const int lane = WARP_ROW ? (threadIdx.x & 31) : threadIdx.x;
+  const int nt = WARP_ROW ? 32 : blockDim.x;
+  const int row = WARP_ROW ? blockIdx.x * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (WARP_ROW && row >= a.T) return;
+  const int nc = a.d >> 3;
+  float r[CH][8];          // the stream, then r
+  uint4 yv[CH], gv[CH];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = lane + i * nt;
+    const bool live = c < nc;
+    if (F32) {
+      if (live) {
+        load8f(static_cast<const float*>(a.x) + row * a.x_ld + 8 * c, r[i]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[i][j] = 0.f;
+      }
+    } else {
+      const uint4 xv = live ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) +
+                                                              row * a.x_ld + 8 * c)
+                            : make_uint4(0, 0, 0, 0);
+      unpack8(xv, r[i]);
+    }
+    yv[i] = gv[i] = make_uint4(0, 0, 0, 0);
+    if (a.y && live) yv[i] = *reinterpret_cast<const uint4*>(a.y + row * a.y_ld + 8 * c);
+    if (a.gate_kind >= MOE_GATE_CHANNEL && live)
+      gv[i] = *reinterpret_cast<const uint4*>(
+          a.gate + (a.gate_kind == MOE_GATE_FULL ? row * a.gate_ld : 0ll) + 8 * c);
+  }
+  float gt = 1.f;
+  if (a.gate_kind == MOE_GATE_TOKEN) {
+    gt = bf16_bits_to_float(a.gate[row]);
+    if (a.sigmoid) gt = 1.f / (1.f + expf(-gt));
+  }
+  float inv_y = 1.f;
+  if (a.post) {
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      float v[8];
+      unpack8(yv[i], v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
+    }
+    inv_y = rsqrtf(row_sum<WARP_ROW>(ss, red[0]) / (float)a.d + a.eps);
+  }
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = lane + i * nt;
+    float u[8], g[8];
+    unpack8(yv[i], u);
+    if (a.post) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) u[j] *= inv_y;
+      if (a.post_w && c < nc) {
+        float w[8];
+        load8f(a.post_w + 8 * c, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] *= w[j] + a.w_off;
+      }
+    }
+    if (a.gate_kind >= MOE_GATE_CHANNEL) {
+      unpack8(gv[i], g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) u[j] *= a.sigmoid ? 1.f / (1.f + expf(-g[j])) : g[j];
+    } else if (a.gate_kind == MOE_GATE_TOKEN) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) u[j] *= gt;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float x = a.a * r[i][j];
+      r[i][j] = a.y ? fmaf(a.b, u[j], x) : x;
+      ss = fmaf(r[i][j], r[i][j], ss);
+    }
+    if (a.x_out && c < nc) {
+      if (F32) {
+        float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.x_out) + row * a.x_out_ld + 8 * c);
+        o[0] = make_float4(r[i][0], r[i][1], r[i][2], r[i][3]);
+        o[1] = make_float4(r[i][4], r[i][5], r[i][6], r[i][7]);
+      } else {
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.x_out) + row * a.x_out_ld + 8 * c) =
+            pack8(r[i]);
+      }
+    }
+  }
+  if (!a.h && !a.codes) return;
+  const float inv = rsqrtf(row_sum<WARP_ROW>(ss, red[1]) / (float)a.d + a.eps);
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = lane + i * nt;
+    const bool live = c < nc;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r[i][j] *= inv;
+    if (a.pre_w && live) {
+      float w[8];
+      load8f(a.pre_w + 8 * c, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) r[i][j] *= w[j] + a.w_off;
+    }
+    if (a.h && live) *reinterpret_cast<uint4*>(a.h + row * a.h_ld + 8 * c) = pack8(r[i]);
+    if (a.codes)
+      quant8(r[i], live, a.codes + (long long)row * a.d + 8 * c,
+             a.scales + (long long)row * blocks128(a.d) + (c >> 4));
+  }
+}
+
+// bf16 rows to e4m3: one half-warp per 128 columns.
+__global__ void __launch_bounds__(256) fp8_quant_kernel(const uint16_t* __restrict__ x, long long ld,
+                                                        int T, int d, uint8_t* __restrict__ codes,
+                                                        float* __restrict__ scales) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int kb = blocks128(d);
+  const long long n = (long long)T * kb;
+  const long long step = (long long)gridDim.x * (blockDim.x >> 4);
+  const int l = threadIdx.x & 15;
+  // whole warps walk the loop: the two halves of a warp differ by one block
+  for (long long b0 = (long long)blockIdx.x * (blockDim.x >> 4) + ((threadIdx.x >> 5) << 1); b0 < n;
+       b0 += step) {
+    const long long b = b0 + ((threadIdx.x >> 4) & 1);
+    const long long row = b / kb;
+    const int cb = (int)(b - row * kb), c = cb * kBlock128 + 8 * l;
+    const bool live = b < n && c < d;
+    float v[8];
+    unpack8(live ? *reinterpret_cast<const uint4*>(x + row * ld + c) : make_uint4(0, 0, 0, 0), v);
+    quant8(v, live, codes + row * d + c, scales + b);
+  }
+}
+
+template <bool F32, bool WARP_ROW, int CH>
+cudaError_t launch_norm(const NormArgs& a, int threads, cudaStream_t st) {
+  const int grid = WARP_ROW ? (a.T + kWarpRows - 1) / kWarpRows : a.T;
+  return launch_pdl(norm_block_kernel<F32, WARP_ROW, CH>, dim3(grid), dim3(threads), 0, st, a);
+}
+
+template <bool F32>
+cudaError_t launch_norm_t(const NormArgs& a, cudaStream_t st) {
+  const int nc = a.d >> 3;
+  if (nc <= 32) return launch_norm<F32, true, 1>(a, 32 * kWarpRows, st);
+  if (nc <= 64) return launch_norm<F32, true, 2>(a, 32 * kWarpRows, st);
+  if (nc <= 128) return launch_norm<F32, true, 4>(a, 32 * kWarpRows, st);
+  return launch_norm<F32, false, 1>(a, (nc + 31) / 32 * 32, st);
+}
+
+}  // namespace
+
+cudaError_t launch_norm_block(const NormArgs& a, bool stream_f32, cudaStream_t st) {
+  return stream_f32 ? launch_norm_t<true>(a, st) : launch_norm_t<false>(a, st);
+}
+
+cudaError_t launch_fp8_quant(const uint16_t* x, long long ld, int T, int d, uint8_t* codes,
+                             float* scales, cudaStream_t st) {
+  const long long n = (long long)T * blocks128(d);
+  long long grid = (n + 15) / 16;
+  if (grid > 8ll * sm_count()) grid = 8ll * sm_count();
+  return launch_pdl(fp8_quant_kernel, dim3((unsigned)grid), dim3(256), 0, st, x, ld, T, d, codes,
+                    scales);
+}
+
+}  // namespace moe
