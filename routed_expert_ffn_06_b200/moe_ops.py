@@ -19,7 +19,12 @@ import ctypes
 import torch
 
 from . import moe
-from .moe import MoEError, _check, _ptr, _stream
+from .moe import MoEError, _check, _ptr
+
+# The current device and a device's current stream as plain integers: torch's
+# public calls build objects on the way (3 us for a stream, as long as a launch).
+_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 NORM_F_POST = 1
 NORM_F_ZERO_CENTRED = 2
@@ -89,20 +94,31 @@ _F32 = (torch.float32,)
 _I32 = (torch.int32,)
 
 
-def _need(t, name, dtypes, shape=None, rows_only=False):
-    """Check one tensor: on the current device, of one of dtypes, of the shape
-    given, dense (or, with rows_only, rows dense and any row pitch)."""
+def _stream(stream, dev):
+    if stream is None:
+        return _raw_stream(dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _need(t, name, dtypes, shape, dev, rows_only=False):
+    """Check one tensor: on the current device `dev`, of one of dtypes, of the
+    shape given, dense (or, with rows_only, rows dense and any row pitch).
+    Returns its address."""
+    if t.dtype in dtypes and t.get_device() == dev and t.shape == shape and (
+            t.is_contiguous() or (rows_only and (t.shape[1] == 1 or t.stride(1) == 1))):
+        return t.data_ptr()
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: {t.dtype}, expected {' or '.join(map(str, dtypes))}")
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    if t.get_device() != dev:
         raise ValueError(f"{name}: on {t.device}, not on the current CUDA device")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if rows_only:
-        if t.shape[1] > 1 and t.stride(1) != 1:
-            raise ValueError(f"{name}: rows are not dense")
-    elif not t.is_contiguous():
-        raise ValueError(f"{name}: not contiguous")
+    raise ValueError(f"{name}: {'rows are not dense' if rows_only else 'not contiguous'}")
+
+
+def _current():
+    """The current CUDA device, -2 (no tensor's) where there is none."""
+    return _device() if torch.cuda.is_initialized() else -2
 
 
 def _blocks(n: int) -> int:
@@ -129,7 +145,7 @@ def make_norm(d: int, pre_w=None, post_w=None, post: bool = False, gate: str = "
         raise ValueError(f"gate {gate!r} / {gate_act!r}")
     for name, w in (("pre_w", pre_w), ("post_w", post_w)):
         if w is not None:
-            _need(w, name, _F32, (d,))
+            _need(w, name, _F32, (d,), _current())
     flags = ((NORM_F_POST if post else 0) | (NORM_F_ZERO_CENTRED if zero_centred else 0)
              | (NORM_F_STREAM_F32 if stream_f32 else 0)
              | (NORM_F_SIGMOID if gate_act == "sigmoid" else 0))
@@ -142,31 +158,34 @@ def moe_norm_block(n: _Handle, x, y, gate, T: int, x_out=None, h=None, codes=Non
     """The norms after one block and before the next (include/moe_ops.h).  x,
     y, gate ("full"), x_out, h: [T, d] with dense rows and any row pitch the
     library takes; y may be None."""
-    s, ref = n.struct, n.ref
+    s, ref, dev = n.struct, n.ref, _current()
     d, kind = s.d, s.gate_kind
-    sdt = _F32 if s.flags & NORM_F_STREAM_F32 else _BF16
-    pitched = {}
-    for name, t, dt in (("x", x, sdt), ("y", y, _BF16), ("gate", gate if kind == 3 else None, _BF16),
-                        ("x_out", x_out, sdt), ("h", h, _BF16)):
-        if t is not None:
-            _need(t, name, dt, (T, d), True)
-            if T > 1 and t.stride(0) != d:
-                pitched[name + "_ld"] = t.stride(0)
-    if pitched:   # the handle itself is never written: calls may share it
-        s = moe_norm.from_buffer_copy(s)
-        for name, v in pitched.items():
-            setattr(s, name, v)
-        ref = ctypes.addressof(s)
-    if gate is not None and kind in (1, 2):
-        _need(gate, "gate", _BF16, (T,) if kind == 1 else (d,))
-    if codes is not None:
-        _need(codes, "codes", _E4M3, (T, d))
-    if scales is not None:
-        _need(scales, "scales", _F32, (T, _blocks(d)))
+    sdt, rows = _F32 if s.flags & NORM_F_STREAM_F32 else _BF16, (T, d)
+    px = _need(x, "x", sdt, rows, dev, True)
+    py = None if y is None else _need(y, "y", _BF16, rows, dev, True)
+    pg = None
+    if gate is not None and kind:
+        pg = _need(gate, "gate", _BF16, rows if kind == 3 else (T,) if kind == 1 else (d,), dev,
+                   kind == 3)
+    po = None if x_out is None else _need(x_out, "x_out", sdt, rows, dev, True)
+    ph = None if h is None else _need(h, "h", _BF16, rows, dev, True)
+    pc = None if codes is None else _need(codes, "codes", _E4M3, rows, dev)
+    ps = None if scales is None else _need(scales, "scales", _F32, (T, _blocks(d)), dev)
     if T == 0:   # an empty tensor has no address to pass
         return
-    _check(load().moe_norm_block(ref, _ptr(x), _ptr(y), _ptr(gate), T, _ptr(x_out), _ptr(h),
-                                 _ptr(codes), _ptr(scales), _stream(stream)), "moe_norm_block")
+    if T > 1:
+        pitched = {}
+        for name, t in (("x_ld", x), ("y_ld", y), ("gate_ld", gate if kind == 3 else None),
+                        ("x_out_ld", x_out), ("h_ld", h)):
+            if t is not None and t.stride(0) != d:
+                pitched[name] = t.stride(0)
+        if pitched:   # the handle itself is never written: calls may share it
+            s = moe_norm.from_buffer_copy(s)
+            for name, v in pitched.items():
+                setattr(s, name, v)
+            ref = ctypes.addressof(s)
+    _check(load().moe_norm_block(ref, px, py, pg, T, po, ph, pc, ps, _stream(stream, dev)),
+           "moe_norm_block")
 
 
 # ---------------------------------------------------------------- products
@@ -175,9 +194,9 @@ def make_fp8_mat(codes, scales) -> _Handle:
     scales [(G,) ceil(N/128), ceil(K/128)]."""
     if codes.dim() not in (2, 3):
         raise ValueError("codes: [N, K] or [G, N, K]")
-    lead, (N, K) = tuple(codes.shape[:-2]), codes.shape[-2:]
-    _need(codes, "codes", _E4M3)
-    _need(scales, "scales", _F32, lead + (_blocks(N), _blocks(K)))
+    lead, (N, K), dev = tuple(codes.shape[:-2]), codes.shape[-2:], _current()
+    _need(codes, "codes", _E4M3, codes.shape, dev)
+    _need(scales, "scales", _F32, lead + (_blocks(N), _blocks(K)), dev)
     return _Handle(moe_fp8_mat(N, K, lead[0] if lead else 1, _ptr(codes), _ptr(scales)), codes,
                    scales)
 
@@ -186,40 +205,43 @@ def moe_fp8_quant(x, codes, scales, stream=None) -> None:
     """bf16 rows [T, d] to e4m3 codes [T, d] and scales [T, ceil(d/128)]."""
     if x.dim() != 2:
         raise ValueError("x: [T, d]")
-    T, d = x.shape
-    _need(x, "x", _BF16, rows_only=True)
-    _need(codes, "codes", _E4M3, (T, d))
-    _need(scales, "scales", _F32, (T, _blocks(d)))
+    (T, d), dev = x.shape, _current()
+    px = _need(x, "x", _BF16, x.shape, dev, True)
+    pc = _need(codes, "codes", _E4M3, (T, d), dev)
+    ps = _need(scales, "scales", _F32, (T, _blocks(d)), dev)
     if T == 0:
         return
-    _check(load().moe_fp8_quant(_ptr(x), x.stride(0) if T > 1 else 0, T, d, _ptr(codes),
-                                _ptr(scales), _stream(stream)), "moe_fp8_quant")
+    _check(load().moe_fp8_quant(px, x.stride(0) if T > 1 else 0, T, d, pc, ps,
+                                _stream(stream, dev)), "moe_fp8_quant")
 
 
-def _products(w, a, a_scales, M, c):
+def _products(w, a, a_scales, M, c, dev):
     s = w.struct
-    _need(a, "a", _E4M3, (M, s.k))
-    _need(a_scales, "a_scales", _F32, (M, _blocks(s.k)))
-    _need(c, "c", _BF16, (M, s.n))
+    k = s.k
+    return (_need(a, "a", _E4M3, (M, k), dev),
+            _need(a_scales, "a_scales", _F32, (M, (k + 127) // 128), dev),
+            _need(c, "c", _BF16, (M, s.n), dev))
 
 
 def moe_fp8_gemm(w: _Handle, a, a_scales, M: int, c, ws=None, stream=None) -> None:
     """c = (a * a_scales) (w * w_scales)^T in bf16 (include/moe_ops.h)."""
-    _products(w, a, a_scales, M, c)
+    dev = _current()
+    pa, psa, pc = _products(w, a, a_scales, M, c, dev)
     if M == 0:
         return
-    _check(load().moe_fp8_gemm(w.ref, _ptr(a), _ptr(a_scales), M, _ptr(c), _ptr(ws),
-                               _stream(stream)), "moe_fp8_gemm")
+    _check(load().moe_fp8_gemm(w.ref, pa, psa, M, pc, _ptr(ws), _stream(stream, dev)),
+           "moe_fp8_gemm")
 
 
 def moe_fp8_gemm_grouped(w: _Handle, a, a_scales, M: int, offsets, c, ws=None, stream=None) -> None:
     """The same with group g's matrix for rows offsets[g] <= m < offsets[g+1]."""
-    _products(w, a, a_scales, M, c)
-    _need(offsets, "offsets", _I32, (w.struct.groups + 1,))
+    dev = _current()
+    pa, psa, pc = _products(w, a, a_scales, M, c, dev)
+    po = _need(offsets, "offsets", _I32, (w.struct.groups + 1,), dev)
     if M == 0:
         return
-    _check(load().moe_fp8_gemm_grouped(w.ref, _ptr(a), _ptr(a_scales), M, _ptr(offsets), _ptr(c),
-                                       _ptr(ws), _stream(stream)), "moe_fp8_gemm_grouped")
+    _check(load().moe_fp8_gemm_grouped(w.ref, pa, psa, M, po, pc, _ptr(ws), _stream(stream, dev)),
+           "moe_fp8_gemm_grouped")
 
 
 # ------------------------------------------------------------------- layer
@@ -233,19 +255,19 @@ def make_fp8_layer(top_k: int, router_w, router_bias, gate_up, gate_up_scales, d
     E, d = router_w.shape
     F = gate_up.shape[-2]
     Fs = 0 if shared_gate_up is None else shared_gate_up.shape[-2]
-    kd, kf, ks = _blocks(d), _blocks(F), _blocks(Fs)
-    _need(router_w, "router_w", _F32)
+    kd, kf, ks, dev = _blocks(d), _blocks(F), _blocks(Fs), _current()
+    _need(router_w, "router_w", _F32, (E, d), dev)
     if router_bias is not None:
-        _need(router_bias, "router_bias", _F32, (E,))
-    _need(gate_up, "gate_up", _E4M3, (E, 2, F, d))
-    _need(gate_up_scales, "gate_up_scales", _F32, (E, 2, kf, kd))
-    _need(down, "down", _E4M3, (E, d, F))
-    _need(down_scales, "down_scales", _F32, (E, kd, kf))
+        _need(router_bias, "router_bias", _F32, (E,), dev)
+    _need(gate_up, "gate_up", _E4M3, (E, 2, F, d), dev)
+    _need(gate_up_scales, "gate_up_scales", _F32, (E, 2, kf, kd), dev)
+    _need(down, "down", _E4M3, (E, d, F), dev)
+    _need(down_scales, "down_scales", _F32, (E, kd, kf), dev)
     if Fs:
-        _need(shared_gate_up, "shared_gate_up", _E4M3, (2, Fs, d))
-        _need(shared_gate_up_scales, "shared_gate_up_scales", _F32, (2, ks, kd))
-        _need(shared_down, "shared_down", _E4M3, (d, Fs))
-        _need(shared_down_scales, "shared_down_scales", _F32, (kd, ks))
+        _need(shared_gate_up, "shared_gate_up", _E4M3, (2, Fs, d), dev)
+        _need(shared_gate_up_scales, "shared_gate_up_scales", _F32, (2, ks, kd), dev)
+        _need(shared_down, "shared_down", _E4M3, (d, Fs), dev)
+        _need(shared_down_scales, "shared_down_scales", _F32, (kd, ks), dev)
     keep = (router_w, router_bias, gate_up, gate_up_scales, down, down_scales, shared_gate_up,
             shared_gate_up_scales, shared_down, shared_down_scales)
     return _Handle(moe_fp8_layer(d, E, F, top_k, Fs, *map(_ptr, keep)), *keep)
@@ -268,15 +290,12 @@ def alloc_fp8_workspace(layer: _Handle, max_tokens: int, device=None) -> torch.T
 
 def moe_fp8_layer_forward(layer: _Handle, x, T: int, y, ws, ids=None, w=None, stream=None) -> None:
     """The whole layer for up to FP8_LAYER_MAX_T tokens (include/moe_ops.h)."""
-    s = layer.struct
-    _need(x, "x", _BF16, (T, s.d_model))
-    _need(y, "y", _BF16, (T, s.d_model))
-    if ids is not None:
-        _need(ids, "ids", _I32, (T, s.top_k))
-    if w is not None:
-        _need(w, "w", _F32, (T, s.top_k))
+    s, dev = layer.struct, _current()
+    px = _need(x, "x", _BF16, (T, s.d_model), dev)
+    py = _need(y, "y", _BF16, (T, s.d_model), dev)
+    pi = None if ids is None else _need(ids, "ids", _I32, (T, s.top_k), dev)
+    pw = None if w is None else _need(w, "w", _F32, (T, s.top_k), dev)
     if T == 0:
         return
-    _check(load().moe_fp8_layer_forward(layer.ref, _ptr(x), T, _ptr(y), _ptr(ids), _ptr(w),
-                                        _ptr(ws), ws.numel(), _stream(stream)),
-           "moe_fp8_layer_forward")
+    _check(load().moe_fp8_layer_forward(layer.ref, px, T, py, pi, pw, _ptr(ws), ws.numel(),
+                                        _stream(stream, dev)), "moe_fp8_layer_forward")

@@ -12,8 +12,8 @@
 //
 // A tile is 128 rows x BN columns.  Warp 0 loads the A and W tiles of each
 // block by TMA (128-byte swizzle: a row of a block is exactly one 128-byte
-// atom), one lane of warp 1 issues the MMAs, warps 2-9 promote: two warps per
-// TMEM lane quarter, each with half of the columns.  TMEM holds 512 / BN
+// atom), one lane of warp 1 issues the MMAs, the other warps promote: two (BN = 256:
+// four) per TMEM lane quarter, each with its part of the columns.  TMEM holds 512 / BN
 // accumulators (two at BN = 256), so the MMAs of the next block run while one
 // is promoted.  Blocks are persistent over tiles.
 //
@@ -34,27 +34,41 @@ constexpr int FG_BM = 128;
 constexpr int FG_BK = kBlock128;                 // bytes = codes
 constexpr int FG_EPI_WARPS = 8;
 constexpr int FG_THREADS = 32 * (2 + FG_EPI_WARPS);
-constexpr int FG_A_BYTES = FG_BM * FG_BK;
 
-template <int BN>
+// One tile shape: BN columns; AR rows of A staged (32: every tile has at most
+// 32 rows, and what the MMA reads as rows 32..127 is whatever follows in shared
+// memory, which only reaches accumulator rows that are never stored); KBS
+// k-blocks per stage of the ring and per group of accumulators.  A hand-over
+// between two roles costs about 200 cycles of barrier operations whatever it
+// hands over, so narrow tiles, whose k-block takes less than that, hand over
+// several at a time.
+template <int BN, int AR>
 struct FgCfg {
-  static constexpr int kStage = FG_A_BYTES + BN * FG_BK;
-  static constexpr int kStages = BN >= 256 ? 4 : BN >= 128 ? 5 : 8;
-  static constexpr int kAcc = BN >= 256 ? 2 : BN >= 128 ? 4 : 8;      // TMEM accumulators
-  static constexpr int kAccCols = BN < 32 ? 32 : BN;                  // TMEM column pitch
-  static constexpr int kCols = BN / 2;                                // columns of one warp
-  // output staging of an epilogue warp: 32 rows x kOutCols bf16 (the four
-  // stages of BN = 256 leave room for 32 columns)
-  static constexpr int kOutCols = BN >= 256 ? 32 : kCols;
+  static constexpr int kKbs = BN == 128 ? 2 : AR == 32 ? 4 : 2;
+  static constexpr int kABytes = AR * FG_BK;
+  static constexpr int kBlockBytes = kABytes + BN * FG_BK;            // one k-block
+  static constexpr int kStage = kKbs * kBlockBytes;
+  // the MMA reads 128 rows from the base of a short A tile: the ring's tail
+  // keeps the last k-block's reads inside it
+  static constexpr int kTail = FG_BM * FG_BK > kBlockBytes ? FG_BM * FG_BK - kBlockBytes : 0;
+  static constexpr int kStages = (192 * 1024 - kTail) / kStage;
+  static constexpr int kGroups = 512 / (kKbs * BN) > 4 ? 4 : 512 / (kKbs * BN);
+  static constexpr int kTmemCols = kGroups * kKbs * BN;
+  static constexpr int kCols = BN / 2;                                // columns of one epilogue warp
+  static constexpr int kLd = kCols < 32 ? kCols : 32;                 // columns of one TMEM load
+  // output staging of an epilogue warp: 32 rows x kOutCols bf16
+  static constexpr int kOutCols = kCols < 32 ? kCols : 32;
   static constexpr int kOutBytes = FG_EPI_WARPS * 32 * kOutCols * 2;
+  static constexpr int kRingEnd = kStages * kStage + kTail;
   static constexpr size_t smem(int G) {
-    return 1024 + (size_t)kStages * kStage + kOutBytes + (2 * kStages + 2 * kAcc) * 8 + 16 +
+    return 1024 + (size_t)kRingEnd + kOutBytes + (2 * kStages + 2 * kGroups + 1) * 8 + 16 +
            (size_t)(2 * G + 2) * 4;
   }
 };
 
+// A by tiles of 128 rows, and by pieces of 32 rows for tiles with few.
 struct alignas(64) FgMaps {
-  CUtensorMap a, w;
+  CUtensorMap a, a32, w, c;     // c: output by 32 rows x 64 columns (pairs of blocks only)
 };
 
 __device__ __forceinline__ void fg_tma_2d(void* dst, const CUtensorMap* map, int c0, int c1,
@@ -75,6 +89,38 @@ __device__ __forceinline__ void fg_mma(uint32_t d_tmem, uint64_t adesc, uint64_t
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+
+// A wait of the running pipeline.  The warps that wait stay whole without
+// voting on the outcome (a vote costs about 60 cycles, as much as the wait
+// itself): a wait that runs out (moe.h's limit; the timer is only read after
+// kPolls polls) records the error and raises the block's `gave_up` flag, and from
+// then on every wait of the block returns at once.  The roles then run to
+// their ends on whatever the memory holds; the outputs are undefined, no copy or
+// MMA outlives the block (fg_drain).
+constexpr int kPolls = 4096;
+__device__ __forceinline__ void fg_wait(uint64_t* bar, uint32_t parity, Control* ctl,
+                                        uint32_t where, uint32_t* gave_up) {
+  if (mbar_try_wait(bar, parity)) return;
+  for (int i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return;
+    if ((i & 63) == 0) {
+      if (*reinterpret_cast<volatile uint32_t*>(gave_up)) return;
+      if (i >= kPolls) {
+        if (!mbar_wait(bar, parity, ctl, where)) *reinterpret_cast<volatile uint32_t*>(gave_up) = 1u;
+        return;
+      }
+    }
+  }
+}
+
+// Copies in flight when a block gave up may count on barriers that it can no
+// longer follow: it outlives them by time.
+__device__ __forceinline__ void fg_drain(const uint32_t* gave_up) {
+  if (*reinterpret_cast<const volatile uint32_t*>(gave_up)) {
+    const unsigned long long t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < kWaitFloorNs) __nanosleep(1000);
+  }
 }
 
 template <int N>
@@ -99,6 +145,37 @@ __device__ __forceinline__ void fg_tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
   }
 }
 
+// Wait for this thread's TMEM loads; v passes through, so that nothing that
+// uses it can move ahead of the wait.
+template <int N>
+__device__ __forceinline__ void fg_tmem_wait(uint32_t (&v)[N]) {
+  if constexpr (N == 32) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
+                   "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]),
+                   "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]),
+                   "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
+                   "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]),
+                   "+r"(v[30]), "+r"(v[31])::"memory");
+  } else if constexpr (N == 16) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
+                   "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]),
+                   "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])::"memory");
+  } else {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
+                   "+r"(v[6]), "+r"(v[7])::"memory");
+  }
+}
+
+// Hand an accumulator back.  Relaxed: the TMEM loads are complete (wait::ld)
+// and nothing else is handed over, while a release would first wait for the
+// scale loads in flight (about 1,000 cycles at cluster scope).
+__device__ __forceinline__ void fg_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
 // acc += s * p on a pair of floats.
 __device__ __forceinline__ void fma2(float2& acc, float2 p, float2 s) {
   unsigned long long a = *reinterpret_cast<unsigned long long*>(&acc);
@@ -118,8 +195,8 @@ struct FgTile {
 
 // Tiles run along the rows of one column stripe first inside a group, so that
 // neighbouring blocks share the weights of the stripe.
-__device__ __forceinline__ bool fg_tile(long long t, const GemmArgs& a, int bn, const int* rows,
-                                        const int* first, FgTile* o) {
+__device__ __forceinline__ bool fg_tile(long long t, const GemmArgs& a, int bm, int bn,
+                                        const int* rows, const int* first, FgTile* o) {
   const int nt = (a.N + bn - 1) / bn;
   if (t >= (long long)first[a.G] * nt) return false;
   // the last group g with first[g] * nt <= t
@@ -133,58 +210,23 @@ __device__ __forceinline__ bool fg_tile(long long t, const GemmArgs& a, int bn, 
   const int mt = first[lo + 1] - first[lo];
   const int q = (int)(t - (long long)first[lo] * nt);
   o->g = lo;
-  o->m0 = rows[lo] + (q % mt) * FG_BM;
+  o->m0 = rows[lo] + (q % mt) * bm;
   o->m_end = rows[lo + 1];
   o->n0 = (q / mt) * bn;
   return true;
 }
 
-template <int BN>
-__global__ void __launch_bounds__(FG_THREADS, 1) fp8_gemm_kernel(
-    GemmArgs a, const __grid_constant__ FgMaps mp) {
-  using C = FgCfg<BN>;
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* smem = reinterpret_cast<unsigned char*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  unsigned char* out_s = smem + C::kStages * C::kStage;
-  uint64_t* full = reinterpret_cast<uint64_t*>(out_s + C::kOutBytes);
-  uint64_t* empty = full + C::kStages;
-  uint64_t* accf = empty + C::kStages;
-  uint64_t* acce = accf + C::kAcc;
-  uint32_t* holder = reinterpret_cast<uint32_t*>(acce + C::kAcc);
-  int* rows = reinterpret_cast<int*>(holder + 4);    // [G+1] first row of each group
-  int* first = rows + a.G + 1;                       // [G+1] first row tile of each group
+// Row range and row-tile count (tiles of bm rows) of each group, into shared
+// memory; the caller's barrier follows.
+__device__ __forceinline__ void fg_groups(const GemmArgs& a, int* rows, int* first,
+                                          int bm = FG_BM) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int KB = blocks128(a.K);
-
-  if (tid == 0) {
-    for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
-    }
-    for (int s = 0; s < C::kAcc; ++s) {
-      mbar_init(&accf[s], 1);
-      mbar_init(&acce[s], FG_EPI_WARPS);
-    }
-    fence_barrier_init();
-  }
-  if (warp == 1) {
-    tmem_alloc(holder, C::kAcc * C::kAccCols);
-    tmem_relinquish();
-  }
-  if (warp == 0 && lane < 2)
-    asm volatile("prefetch.tensormap [%0];" ::"l"(
-                     reinterpret_cast<uint64_t>(lane == 0 ? &mp.a : &mp.w))
-                 : "memory");
-  pdl_wait();
-  pdl_launch_dependents();
-  // row range and row-tile count of each group
   if (!a.offsets) {
     if (tid == 0) {
       rows[0] = 0;
       rows[1] = a.M;
       first[0] = 0;
-      first[1] = (a.M + FG_BM - 1) / FG_BM;
+      first[1] = (a.M + bm - 1) / bm;
     }
   } else if (warp == 0) {
     // one warp scans the offsets: a running maximum clamps them to 0..M and to
@@ -205,7 +247,7 @@ __global__ void __launch_bounds__(FG_THREADS, 1) fp8_gemm_kernel(
       int prev = __shfl_up_sync(0xffffffffu, v, 1);
       if (lane == 0) prev = top;
       // tiles of group g - 1 end at offset g
-      int n = (g >= 1 && g <= a.G) ? (v - prev + FG_BM - 1) / FG_BM : 0;
+      int n = (g >= 1 && g <= a.G) ? (v - prev + bm - 1) / bm : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int u = __shfl_up_sync(0xffffffffu, n, o);
@@ -221,93 +263,218 @@ __global__ void __launch_bounds__(FG_THREADS, 1) fp8_gemm_kernel(
     if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0)
       record_error(a.ctl, kErrRange, 0x400);
   }
+}
+
+// One epilogue warp's 32 rows x COLS columns to bf16 and to global memory,
+// through its staging buffer of OUT columns at a time (16-byte pieces, rotated
+// by the row so that neither side conflicts), so that stores cover whole runs
+// of a row.
+template <int COLS, int OUT>
+__device__ __forceinline__ void fg_store(const GemmArgs& a, const float2 (&acc)[COLS / 2],
+                                         uint32_t* stage, int row0, int nrow, int col0, int lane) {
+  constexpr int PIECES = OUT / 8;     // 16-byte pieces of a staged row
+  constexpr int RPI = 32 / PIECES;    // rows of one store instruction
+  const bool vec = (a.N & 7) == 0 && (reinterpret_cast<uintptr_t>(a.c) & 15) == 0;
+#pragma unroll
+  for (int c = 0; c < COLS; c += OUT) {
+    __syncwarp();
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p) {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = acc[(c + 8 * p) / 2 + j];
+        const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
+        w[j] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+      const int at = p ^ (lane & (PIECES - 1));
+      *reinterpret_cast<uint4*>(stage + (lane * PIECES + at) * 4) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __syncwarp();
+    const int cols = min(OUT, a.N - (col0 + c));
+    if (vec) {
+      const int p = lane % PIECES, r0 = lane / PIECES;
+      uint16_t* o = a.c + (long long)(row0 + r0) * a.N + col0 + c + 8 * p;
+      const long long step = (long long)RPI * a.N;
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i, o += step) {
+        const int r = r0 + i * RPI;
+        if (r < nrow && 8 * p < cols)
+          *reinterpret_cast<uint4*>(o) =
+              *reinterpret_cast<const uint4*>(stage + (r * PIECES + (p ^ (r & (PIECES - 1)))) * 4);
+      }
+    } else {
+      const uint16_t* s16 = reinterpret_cast<const uint16_t*>(stage);
+      for (int i = lane; i < 32 * OUT; i += 32) {
+        const int r = i / OUT, n = i % OUT, p = n >> 3;
+        if (r < nrow && n < cols)
+          a.c[(long long)(row0 + r) * a.N + col0 + c + n] =
+              s16[(r * PIECES + (p ^ (r & (PIECES - 1)))) * 8 + (n & 7)];
+      }
+    }
+  }
+}
+
+template <int BN, int AR>
+__global__ void __launch_bounds__(FG_THREADS, 1) fp8_gemm_kernel(
+    GemmArgs a, const __grid_constant__ FgMaps mp) {
+  using C = FgCfg<BN, AR>;
+  constexpr int KBS = C::kKbs;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  unsigned char* out_s = smem + C::kRingEnd;
+  uint64_t* full = reinterpret_cast<uint64_t*>(out_s + C::kOutBytes);
+  uint64_t* empty = full + C::kStages;
+  uint64_t* accf = empty + C::kStages;
+  uint64_t* acce = accf + C::kGroups;
+  uint64_t* done = acce + C::kGroups;                // every MMA has completed
+  uint32_t* holder = reinterpret_cast<uint32_t*>(done + 1);
+  uint32_t* gave_up = holder + 1;
+  int* rows = reinterpret_cast<int*>(holder + 4);    // [G+1] first row of each group
+  int* first = rows + a.G + 1;                       // [G+1] first row tile of each group
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int KB = blocks128(a.K);
+
+  if (tid == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < C::kGroups; ++s) {
+      mbar_init(&accf[s], 1);
+      mbar_init(&acce[s], FG_EPI_WARPS);
+    }
+    mbar_init(done, 1);
+    *gave_up = 0u;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(holder, C::kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == 0 && lane < 3)
+    asm volatile("prefetch.tensormap [%0];" ::"l"(
+                     reinterpret_cast<uint64_t>(lane == 0 ? &mp.a : lane == 1 ? &mp.a32 : &mp.w))
+                 : "memory");
+  pdl_wait();
+  pdl_launch_dependents();
+  fg_groups(a, rows, first);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *holder;
+  const bool elected = elect_one();
 
+  // The loader and the MMA warp walk their loops whole, with one lane, elected
+  // once, issuing, so that the loop's values stay warp-uniform (a loop under
+  // lane == 0 spent twice the cycles on issuing).
   if (warp == 0) {
-    if (lane == 0) {
-      int s = 0;
-      uint32_t ph = 0;
-      long long fills = 0;
-      bool ok = true;
-      FgTile tl;
-      for (long long t = blockIdx.x; ok && fg_tile(t, a, BN, rows, first, &tl); t += gridDim.x) {
-        const int wrow = tl.g * a.N + tl.n0;
-        for (int kb = 0; kb < KB; ++kb) {
-          if (fills >= C::kStages && !mbar_wait(&empty[s], ph ^ 1u, a.ctl, 0x401)) {
-            ok = false;
-            break;
-          }
-          unsigned char* st = smem + s * C::kStage;
-          mbar_arrive_expect_tx(&full[s], C::kStage);
-          fg_tma_2d(st, &mp.a, kb * FG_BK, tl.m0, &full[s]);
-          fg_tma_2d(st + FG_A_BYTES, &mp.w, kb * FG_BK, wrow, &full[s]);
+    int s = 0;
+    uint32_t ph = 0;
+    int fills = 0;          // capped at kStages
+    long long n = 0;
+    FgTile tl;
+    for (long long t = blockIdx.x; fg_tile(t, a, FG_BM, BN, rows, first, &tl);
+         t += gridDim.x) {
+      const int wrow = tl.g * a.N + tl.n0;
+      // Rows past the tile's last are not loaded, by pieces of 32.
+      const int nrow = min(FG_BM, tl.m_end - tl.m0), pieces = nrow > 96 ? 0 : (nrow + 31) / 32;
+      const uint32_t bytes = ((pieces ? pieces * 32 : FG_BM) + BN) * FG_BK;
+      for (int kb = 0; kb < KB; kb += KBS) {
+        if (fills == C::kStages) {
+          fg_wait(&empty[s], ph ^ 1u, a.ctl, 0x401, gave_up);
+        } else {
           ++fills;
-          if (++s == C::kStages) {
-            s = 0;
-            ph ^= 1u;
+        }
+        if (elected) {
+          unsigned char* st = smem + s * C::kStage;
+          const int nk = min(KBS, KB - kb);
+          mbar_arrive_expect_tx(&full[s], nk * bytes);
+#pragma unroll
+          for (int j = 0; j < KBS; ++j) {
+            if (j < nk) {
+              unsigned char* b = st + j * C::kBlockBytes;
+              if (AR == FG_BM && pieces == 0) {
+                fg_tma_2d(b, &mp.a, (kb + j) * FG_BK, tl.m0, &full[s]);
+              } else {
+                for (int p = 0; p < (AR == 32 ? 1 : pieces); ++p)
+                  fg_tma_2d(b + p * 32 * FG_BK, &mp.a32, (kb + j) * FG_BK, tl.m0 + 32 * p, &full[s]);
+              }
+              fg_tma_2d(b + C::kABytes, &mp.w, (kb + j) * FG_BK, wrow, &full[s]);
+            }
           }
         }
+        ++n;
+        if (++s == C::kStages) {
+          s = 0;
+          ph ^= 1u;
+        }
       }
-      // the newest phase of each stage may be unconsumed: its copies land first
-      for (long long j = fills > C::kStages ? fills - C::kStages : 0; j < fills; ++j)
-        mbar_wait(&full[j % C::kStages], (uint32_t)(j / C::kStages) & 1u, a.ctl, 0x402);
     }
+    // the newest phase of each stage may be unconsumed: its copies land first
+    for (long long j = n - fills; j < n; ++j)
+      fg_wait(&full[j % C::kStages], (uint32_t)(j / C::kStages) & 1u, a.ctl, 0x402, gave_up);
+    fg_drain(gave_up);
   } else if (warp == 1) {
-    if (lane == 0) {
-      // kind::f8f6f4: e4m3 A and B (format 0), fp32 D, both K-major
-      const uint32_t idesc = idesc_f16_f32(FG_BM, BN);
-      const uint64_t desc0 = sw128_kmajor_desc(smem_u32(smem));
-      int s = 0, as = 0;
-      uint32_t ph = 0, aph = 0;
-      long long issued = 0;
-      bool ok = true;
-      FgTile tl;
-      for (long long t = blockIdx.x; ok && fg_tile(t, a, BN, rows, first, &tl); t += gridDim.x) {
-        for (int kb = 0; kb < KB; ++kb) {
-          if ((issued >= C::kAcc && !mbar_wait(&acce[as], aph ^ 1u, a.ctl, 0x403)) ||
-              !mbar_wait(&full[s], ph, a.ctl, 0x404)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t ad = desc0 + (uint64_t)(s * (C::kStage >> 4));
-          const uint64_t bd = ad + (FG_A_BYTES >> 4);
-          const uint32_t d = tmem + (uint32_t)(as * C::kAccCols);
+    // kind::f8f6f4: e4m3 A and B (format 0), fp32 D, both K-major
+    const uint32_t idesc = idesc_f16_f32(FG_BM, BN);
+    const uint64_t desc0 = sw128_kmajor_desc(smem_u32(smem));
+    int s = 0, as = 0, used = 0;     // used: accumulator groups handed out, capped at kGroups
+    uint32_t ph = 0, aph = 0;
+    FgTile tl;
+    for (long long t = blockIdx.x; fg_tile(t, a, FG_BM, BN, rows, first, &tl);
+         t += gridDim.x) {
+      for (int kb = 0; kb < KB; kb += KBS) {
+        if (used == C::kGroups) {
+          fg_wait(&acce[as], aph ^ 1u, a.ctl, 0x403, gave_up);
+        } else {
+          ++used;
+        }
+        fg_wait(&full[s], ph, a.ctl, 0x404, gave_up);
+        tc_fence_after();
+        if (elected) {
+          const uint64_t st = desc0 + (uint64_t)(s * (C::kStage >> 4));
+          const uint32_t d = tmem + (uint32_t)(as * KBS * BN);
+          const int nk = min(KBS, KB - kb);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) fg_mma(d, ad + 2 * j, bd + 2 * j, idesc, j > 0 ? 1u : 0u);
+          for (int j = 0; j < KBS; ++j) {
+            if (j < nk) {
+              const uint64_t ad = st + (uint64_t)(j * (C::kBlockBytes >> 4));
+              const uint64_t bd = ad + (C::kABytes >> 4);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                fg_mma(d + (uint32_t)(j * BN), ad + 2 * i, bd + 2 * i, idesc, i > 0 ? 1u : 0u);
+            }
+          }
           tc_commit(&empty[s]);
           tc_commit(&accf[as]);
-          ++issued;
-          if (++s == C::kStages) {
-            s = 0;
-            ph ^= 1u;
-          }
-          if (++as == C::kAcc) {
-            as = 0;
-            aph ^= 1u;
-          }
+        }
+        if (++s == C::kStages) {
+          s = 0;
+          ph ^= 1u;
+        }
+        if (++as == C::kGroups) {
+          as = 0;
+          aph ^= 1u;
         }
       }
-      // every MMA issued has completed before this warp frees the TMEM: the
-      // last phase of each accumulator
-      for (long long j = issued > C::kAcc ? issued - C::kAcc : 0; j < issued; ++j)
-        mbar_wait(&accf[j % C::kAcc], (uint32_t)(j / C::kAcc) & 1u, a.ctl, 0x405);
     }
+    // every MMA issued has completed before this warp frees the TMEM
+    if (elected) tc_commit(done);
+    mbar_wait(done, 0, a.ctl, 0x405);
   } else {
-    const int ew = warp - 2, q = warp & 3, half = ew >> 2;
-    const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(half * C::kCols);
+    const int ew = warp - 2, q = warp & 3, part = ew >> 2;
+    const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(part * C::kCols);
     uint32_t* stage = reinterpret_cast<uint32_t*>(out_s + ew * (32 * C::kOutCols * 2));
-    constexpr int LD = C::kCols < 16 ? C::kCols : 16;    // columns of one TMEM load
+    constexpr int LD = C::kLd, CH = C::kCols / LD;     // loads per k-block
     int as = 0;
     uint32_t aph = 0;
-    bool ok = true;
     FgTile tl;
-    for (long long t = blockIdx.x; ok && fg_tile(t, a, BN, rows, first, &tl); t += gridDim.x) {
+    for (long long t = blockIdx.x; fg_tile(t, a, FG_BM, BN, rows, first, &tl);
+         t += gridDim.x) {
       const int row0 = tl.m0 + 32 * q, row = row0 + lane;
-      const int col0 = tl.n0 + half * C::kCols;
+      const int col0 = tl.n0 + part * C::kCols;
       const bool idle = row0 >= tl.m_end || col0 >= a.N;   // nothing of this warp's part is stored
       const float* sa = a.a_scales + (long long)min(row, a.M - 1) * KB;
       const float* sw = a.w_scales +
@@ -315,6 +482,298 @@ __global__ void __launch_bounds__(FG_THREADS, 1) fp8_gemm_kernel(
       float2 acc[C::kCols / 2];
 #pragma unroll
       for (int j = 0; j < C::kCols / 2; ++j) acc[j] = make_float2(0.f, 0.f);
+      // scales of the next group, in flight while the present one is promoted
+      float sa_n[KBS], sw_n[KBS];
+#pragma unroll
+      for (int j = 0; j < KBS; ++j) {
+        sa_n[j] = !idle && j < KB ? sa[j] : 0.f;
+        sw_n[j] = !idle && j < KB ? sw[j] : 0.f;
+      }
+      for (int kb = 0; kb < KB; kb += KBS) {
+        float sc[KBS];
+#pragma unroll
+        for (int j = 0; j < KBS; ++j) {
+          sc[j] = sa_n[j] * sw_n[j];
+          const bool more = !idle && kb + KBS + j < KB;
+          sa_n[j] = more ? sa[kb + KBS + j] : 0.f;
+          sw_n[j] = more ? sw[kb + KBS + j] : 0.f;
+        }
+        fg_wait(&accf[as], aph, a.ctl, 0x406, gave_up);
+        if (!idle) {
+          tc_fence_after();
+          const uint32_t base = lane_base + (uint32_t)(as * KBS * BN);
+          const int nk = min(KBS, KB - kb);
+          // one load ahead of the sums
+          uint32_t v[2][LD];
+          fg_tmem_ld<LD>(base, v[0]);
+#pragma unroll
+          for (int i = 0; i < KBS * CH; ++i) {
+            const int j = i / CH, c = (i % CH) * LD;
+            if (j < nk) {
+              fg_tmem_wait<LD>(v[i & 1]);
+              if (i + 1 < KBS * CH && (i + 1) / CH < nk)
+                fg_tmem_ld<LD>(base + (uint32_t)(((i + 1) / CH) * BN + ((i + 1) % CH) * LD),
+                               v[(i + 1) & 1]);
+              const float2 sc2 = make_float2(sc[j], sc[j]);
+#pragma unroll
+              for (int x = 0; x < LD; x += 2)
+                fma2(acc[(c + x) / 2],
+                     make_float2(__uint_as_float(v[i & 1][x]), __uint_as_float(v[i & 1][x + 1])),
+                     sc2);
+            }
+          }
+          tc_fence_before();
+        }
+        if (elected) fg_arrive(&acce[as]);
+        if (++as == C::kGroups) {
+          as = 0;
+          aph ^= 1u;
+        }
+      }
+      if (idle) continue;
+      fg_store<C::kCols, C::kOutCols>(a, acc, stage, row0, min(32, tl.m_end - row0), col0, lane);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
+}
+
+// ------------------------------------------------------- two SMs on one tile
+// 256 x 256 tiles for many rows: a pair of blocks shares one tcgen05.mma
+// (cta_group::2, M = 256). Each block loads its own 128 rows of A and half of
+// the tile's W, 32 KB per k-block instead of the 48 KB a block of its own would
+// load for the same work: the L2 delivers about 68 bytes per cycle and SM
+// (measured), so 48 KB take 720 cycles and 32 KB take 480, less than the 540 of
+// the MMAs themselves. Both loaders count their bytes on the even block's
+// barriers; the even block's commits release both blocks.
+//
+// A hand-over between roles of two SMs takes some hundred cycles, so a k-block
+// is two MMA groups of 128 columns, each with two TMEM accumulators and four
+// epilogue warps of its own: while one accumulator of a half is read back, its
+// other one and the other half keep the tensor cores busy.  Eight epilogue warps
+// per block hold 128 sums a thread, with the registers that the other warps
+// give up (setmaxnreg).
+constexpr int FP_STAGES = 4;
+constexpr int FP_HALF = FG_BM * FG_BK;                 // 16 KB: 128 rows of a k-block
+constexpr int FP_STAGE = 2 * FP_HALF;
+constexpr int FP_THREADS = 384;                        // 4 warps of roles, 8 of epilogue
+constexpr int FP_SLOTS = 4;                            // TMEM accumulators of 128 columns
+constexpr int FP_OUT_BYTES = FG_EPI_WARPS * 32 * 128 * 2;   // a warp's 32 rows x 128 columns
+constexpr int FP_REGS = 168, FP_REGS_ROLE = 40, FP_REGS_EPI = 232;
+static_assert(4 * FP_REGS_ROLE + 8 * FP_REGS_EPI <= 12 * FP_REGS,
+              "setmaxnreg hands out what the block was launched with");
+
+__host__ __device__ constexpr size_t fp_smem(int G) {
+  return 1024 + (size_t)FP_STAGES * FP_STAGE + FP_OUT_BYTES + (2 * FP_STAGES + 2 * FP_SLOTS + 1) * 8 + 16 +
+         (size_t)(2 * G + 2) * 4;
+}
+
+__device__ __forceinline__ uint32_t fp_even(const void* p) {   // p's place in the even block
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
+  return r;
+}
+__device__ __forceinline__ void fp_cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+// A load whose bytes count on a barrier of the pair's even block.
+__device__ __forceinline__ void fp_tma_2d(void* dst, const CUtensorMap* map, int c0, int c1,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void fp_mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                       uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrive on the barrier at this place of both blocks once the MMAs issued so
+// far have completed.
+__device__ __forceinline__ void fp_commit(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void fp_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP_THREADS, 1)
+    fp8_gemm_pair_kernel(GemmArgs a, const __grid_constant__ FgMaps mp) {
+  constexpr int BM = 256, BN = 256;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  unsigned char* out_s = smem + FP_STAGES * FP_STAGE;
+  uint64_t* full = reinterpret_cast<uint64_t*>(out_s + FP_OUT_BYTES);
+  uint64_t* empty = full + FP_STAGES;
+  uint64_t* accf = empty + FP_STAGES;
+  uint64_t* acce = accf + FP_SLOTS;
+  uint64_t* done = acce + FP_SLOTS;
+  uint32_t* holder = reinterpret_cast<uint32_t*>(done + 1);
+  uint32_t* gave_up = holder + 1;
+  int* rows = reinterpret_cast<int*>(holder + 4);
+  int* first = rows + a.G + 1;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int KB = blocks128(a.K);
+
+  if (tid == 0) {
+    for (int s = 0; s < FP_STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < FP_SLOTS; ++s) {
+      mbar_init(&accf[s], 1);
+      mbar_init(&acce[s], FG_EPI_WARPS);      // four warps of each block
+    }
+    mbar_init(done, 1);
+    *gave_up = 0u;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     smem_u32(holder))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  if (warp == 0 && lane < 3)
+    asm volatile("prefetch.tensormap [%0];" ::"l"(
+                     reinterpret_cast<uint64_t>(lane == 0 ? &mp.a : lane == 1 ? &mp.a32 : &mp.w))
+                 : "memory");
+  pdl_wait();
+  pdl_launch_dependents();
+  fg_groups(a, rows, first, BM);
+  tc_fence_before();
+  __syncthreads();
+  fp_cluster_sync();       // both blocks' barriers are initialised
+  tc_fence_after();
+  const uint32_t tmem = *holder;
+  const bool elected = elect_one();
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FP_REGS_ROLE));
+    if (warp == 0) {
+      int s = 0;
+      uint32_t ph = 0;
+      int fills = 0;
+      long long n = 0;
+      FgTile tl;
+      for (long long t = pair; fg_tile(t, a, BM, BN, rows, first, &tl); t += pairs) {
+        // valid rows of each block's half, loaded by pieces of 32 where few
+        const int r0 = min(FG_BM, tl.m_end - tl.m0), r1 = max(0, min(FG_BM, tl.m_end - tl.m0 - FG_BM));
+        const int p0 = r0 > 96 ? 4 : (r0 + 31) / 32, p1 = r1 > 96 ? 4 : (r1 + 31) / 32;
+        const int mine = rank ? p1 : p0;
+        const uint32_t bytes = (uint32_t)(p0 + p1) * 32 * FG_BK + 2 * FP_HALF;
+        const int arow = tl.m0 + rank * FG_BM, wrow = tl.g * a.N + tl.n0 + rank * 64;
+        for (int kb = 0; kb < KB; ++kb) {
+          if (fills == FP_STAGES) {
+            fg_wait(&empty[s], ph ^ 1u, a.ctl, 0x411, gave_up);
+          } else {
+            ++fills;
+          }
+          if (elected) {
+            unsigned char* st = smem + s * FP_STAGE;
+            const uint32_t bar = fp_even(&full[s]);
+            if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
+            if (mine == 4) {
+              fp_tma_2d(st, &mp.a, kb * FG_BK, arow, bar);
+            } else {
+              for (int p = 0; p < mine; ++p)
+                fp_tma_2d(st + p * 32 * FG_BK, &mp.a32, kb * FG_BK, arow + 32 * p, bar);
+            }
+            // half h of the columns: 64 rows of W in each block
+            fp_tma_2d(st + FP_HALF, &mp.w, kb * FG_BK, wrow, bar);
+            fp_tma_2d(st + FP_HALF + FP_HALF / 2, &mp.w, kb * FG_BK, wrow + 128, bar);
+          }
+          ++n;
+          if (++s == FP_STAGES) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      // the newest phase of each stage may be unconsumed: the copies of both
+      // blocks land before either block ends (the cluster barrier below)
+      if (rank == 0)
+        for (long long j = n - fills; j < n; ++j)
+          fg_wait(&full[j % FP_STAGES], (uint32_t)(j / FP_STAGES) & 1u, a.ctl, 0x412, gave_up);
+      fg_drain(gave_up);
+    } else if (warp == 1 && rank == 0) {
+      const uint32_t idesc = idesc_f16_f32(BM, BN / 2);
+      const uint64_t desc0 = sw128_kmajor_desc(smem_u32(smem));
+      int s = 0, as = 0, used = 0;
+      uint32_t ph = 0, aph = 0;
+      FgTile tl;
+      for (long long t = pair; fg_tile(t, a, BM, BN, rows, first, &tl); t += pairs) {
+        for (int kb = 0; kb < KB; ++kb) {
+          fg_wait(&full[s], ph, a.ctl, 0x414, gave_up);
+          const uint64_t ad = desc0 + (uint64_t)(s * (FP_STAGE >> 4)), bd = ad + (FP_HALF >> 4);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (used == FP_SLOTS) {
+              fg_wait(&acce[as], aph ^ 1u, a.ctl, 0x413, gave_up);
+            } else {
+              ++used;
+            }
+            tc_fence_after();
+            if (elected) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                fp_mma(tmem + (uint32_t)(as * (BN / 2)), ad + 2 * i, bd + 2 * i + h * (FP_HALF >> 5),
+                       idesc, i > 0 ? 1u : 0u);
+              fp_commit(&accf[as]);
+              if (h == 1) fp_commit(&empty[s]);
+            }
+            if (++as == FP_SLOTS) {
+              as = 0;
+              aph ^= 1u;
+            }
+          }
+          if (++s == FP_STAGES) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      // every MMA issued has completed before the pair frees its TMEM
+      if (elected) fp_commit(done);
+      mbar_wait(done, 0, a.ctl, 0x415);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(FP_REGS_EPI));
+    constexpr int COLS = 128, LD = 32;
+    const int ew = warp - 4, q = warp & 3, part = ew >> 2;     // part: the half of the columns
+    const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(part * COLS);
+    unsigned char* stage = out_s + ew * (32 * COLS * 2);
+    const uint32_t free_bar = fp_even(&acce[part]);
+    const bool tma_out = (a.N & 7) == 0 && (reinterpret_cast<uintptr_t>(a.c) & 15) == 0;
+    int as = 0;           // accumulator 2 * as + part
+    uint32_t aph = 0;
+    FgTile tl;
+    for (long long t = pair; fg_tile(t, a, BM, BN, rows, first, &tl); t += pairs) {
+      const int row0 = tl.m0 + rank * FG_BM + 32 * q, row = row0 + lane;
+      const int col0 = tl.n0 + part * COLS;
+      const bool idle = row0 >= tl.m_end || col0 >= a.N;
+      const float* sa = a.a_scales + (long long)min(row, a.M - 1) * KB;
+      const float* sw = a.w_scales +
+                        ((long long)tl.g * blocks128(a.N) + min(col0, a.N - 1) / kBlock128) * KB;
+      float2 acc[COLS / 2];
+#pragma unroll
+      for (int j = 0; j < COLS / 2; ++j) acc[j] = make_float2(0.f, 0.f);
       float sa_n = idle ? 0.f : sa[0], sw_n = idle ? 0.f : sw[0];
       for (int kb = 0; kb < KB; ++kb) {
         const float sc = sa_n * sw_n;
@@ -322,80 +781,82 @@ __global__ void __launch_bounds__(FG_THREADS, 1) fp8_gemm_kernel(
           sa_n = sa[kb + 1];
           sw_n = sw[kb + 1];
         }
-        ok = mbar_wait(&accf[as], aph, a.ctl, 0x406);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+        fg_wait(&accf[2 * as + part], aph, a.ctl, 0x416, gave_up);
         if (!idle) {
           tc_fence_after();
+          const uint32_t base = lane_base + (uint32_t)(as * BN);
           const float2 sc2 = make_float2(sc, sc);
+          uint32_t v[2][LD];
+          fg_tmem_ld<LD>(base, v[0]);
 #pragma unroll
-          for (int c = 0; c < C::kCols; c += LD) {
-            uint32_t v[LD];
-            fg_tmem_ld<LD>(lane_base + (uint32_t)(as * C::kAccCols + c), v);
-            tmem_ld_wait();
+          for (int i = 0; i < COLS / LD; ++i) {
+            fg_tmem_wait<LD>(v[i & 1]);
+            if (i + 1 < COLS / LD) {
+              fg_tmem_ld<LD>(base + (uint32_t)((i + 1) * LD), v[(i + 1) & 1]);
+            } else {
+              // everything is in registers: hand the accumulator back before the last sums
+              tc_fence_before();
+              if (elected) fp_arrive(free_bar + 16 * as);
+            }
 #pragma unroll
-            for (int j = 0; j < LD; j += 2)
-              fma2(acc[(c + j) / 2], make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])),
-                   sc2);
+            for (int x = 0; x < LD; x += 2)
+              fma2(acc[(i * LD + x) / 2],
+                   make_float2(__uint_as_float(v[i & 1][x]), __uint_as_float(v[i & 1][x + 1])), sc2);
           }
-          tc_fence_before();
+        } else if (elected) {
+          fp_arrive(free_bar + 16 * as);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&acce[as]);
-        if (++as == C::kAcc) {
-          as = 0;
-          aph ^= 1u;
-        }
+        as ^= 1;
+        if (as == 0) aph ^= 1u;
       }
-      if (!ok || idle) continue;
-      // rows of this warp to bf16 through its staging buffer (16-byte pieces,
-      // rotated by the row so that neither side conflicts), then rows of
-      // kOutCols columns to global memory
-      constexpr int PIECES = C::kOutCols / 8;     // 16-byte pieces of a staged row
-      const int nrow = min(32, tl.m_end - row0);
-      const bool vec = (a.N & 7) == 0 && (reinterpret_cast<uintptr_t>(a.c) & 15) == 0;
+      if (idle) continue;
+      // the staging buffer is free once the previous tile's store has read it
+      if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      __syncwarp();
+      if (tma_out && (!a.offsets || row0 + 32 <= tl.m_end)) {
+        // a TMA store of 32 rows x 64 columns twice (128-byte swizzle: piece p of
+        // row r at p ^ (r & 7)); the copy clips rows and columns of no product,
+        // and runs while the next tile is summed
 #pragma unroll
-      for (int c = 0; c < C::kCols; c += C::kOutCols) {
-        __syncwarp();
-#pragma unroll
-        for (int p = 0; p < PIECES; ++p) {
+        for (int p = 0; p < COLS / 8; ++p) {
           uint32_t w[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float2 f = acc[(c + 8 * p) / 2 + j];
+            const float2 f = acc[4 * p + j];
             const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
             w[j] = *reinterpret_cast<const uint32_t*>(&b);
           }
-          const int at = p ^ (lane & (PIECES - 1));
-          *reinterpret_cast<uint4*>(stage + (lane * PIECES + at) * 4) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(stage + (p >> 3) * 4096 + lane * 128 +
+                                    (((p & 7) ^ (lane & 7)) << 4)) =
+              make_uint4(w[0], w[1], w[2], w[3]);
         }
+        fence_proxy_async_smem();
         __syncwarp();
-        const int cols = min(C::kOutCols, a.N - (col0 + c));
-        if (vec) {
-#pragma unroll 4
-          for (int i = lane; i < 32 * PIECES; i += 32) {
-            const int r = i / PIECES, p = i % PIECES;
-            if (r < nrow && 8 * p < cols)
-              *reinterpret_cast<uint4*>(a.c + (long long)(row0 + r) * a.N + col0 + c + 8 * p) =
-                  *reinterpret_cast<const uint4*>(stage + (r * PIECES + (p ^ (r & (PIECES - 1)))) * 4);
-          }
-        } else {
-          const uint16_t* s16 = reinterpret_cast<const uint16_t*>(stage);
-          for (int i = lane; i < 32 * C::kOutCols; i += 32) {
-            const int r = i / C::kOutCols, n = i % C::kOutCols, p = n >> 3;
-            if (r < nrow && n < cols)
-              a.c[(long long)(row0 + r) * a.N + col0 + c + n] =
-                  s16[(r * PIECES + (p ^ (r & (PIECES - 1)))) * 8 + (n & 7)];
-          }
+        if (lane == 0) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if (col0 + 64 * h < a.N)
+              asm volatile(
+                  "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                      reinterpret_cast<uint64_t>(&mp.c)),
+                  "r"(col0 + 64 * h), "r"(row0), "r"(smem_u32(stage + h * 4096))
+                  : "memory");
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
         }
+      } else {
+        fg_store<COLS, 64>(a, acc, reinterpret_cast<uint32_t*>(stage), row0,
+                           min(32, tl.m_end - row0), col0, lane);
       }
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  fp_cluster_sync();       // no block ends while the other may still use its memory
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, C::kAcc * C::kAccCols);
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 fg_encode() {
@@ -424,35 +885,93 @@ bool fg_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uin
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN>
+template <int BN, int AR>
 cudaError_t fg_launch(const GemmArgs& a, long long tiles, cudaStream_t st) {
-  FgMaps mp;
+  FgMaps mp = {};
   if (!fg_map(&mp.a, a.a, (uint64_t)a.K, (uint64_t)a.M, FG_BM) ||
+      !fg_map(&mp.a32, a.a, (uint64_t)a.K, (uint64_t)a.M, 32) ||
       !fg_map(&mp.w, a.w, (uint64_t)a.K, (uint64_t)a.N * a.G, BN))
     return cudaErrorInvalidValue;
-  const size_t sm = FgCfg<BN>::smem(a.G);
-  cudaError_t e = cudaFuncSetAttribute(fp8_gemm_kernel<BN>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(fp8_gemm_kernel<BN, AR>));
   if (e != cudaSuccess) return e;
   const long long grid = tiles < sm_count() ? tiles : sm_count();
-  return launch_pdl(fp8_gemm_kernel<BN>, dim3((unsigned)grid), dim3(FG_THREADS), sm, st, a, mp);
+  return launch_pdl(fp8_gemm_kernel<BN, AR>, dim3((unsigned)grid), dim3(FG_THREADS),
+                    FgCfg<BN, AR>::smem(a.G), st, a, mp);
+}
+
+cudaError_t fg_launch_pair(const GemmArgs& a, long long tiles, cudaStream_t st) {
+  FgMaps mp = {};
+  if (!fg_map(&mp.a, a.a, (uint64_t)a.K, (uint64_t)a.M, FG_BM) ||
+      !fg_map(&mp.a32, a.a, (uint64_t)a.K, (uint64_t)a.M, 32) ||
+      !fg_map(&mp.w, a.w, (uint64_t)a.K, (uint64_t)a.N * a.G, 64))
+    return cudaErrorInvalidValue;
+  if ((a.N & 7) == 0 && (reinterpret_cast<uintptr_t>(a.c) & 15) == 0) {
+    cuuint64_t dims[2] = {(cuuint64_t)a.N, (cuuint64_t)a.M}, strides[1] = {(cuuint64_t)a.N * 2};
+    cuuint32_t box[2] = {64, 32}, estr[2] = {1, 1};
+    if (fg_encode()(&mp.c, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.c, dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  // a block launched with fewer registers than the split hands out would wait for ever
+  cudaFuncAttributes at;
+  cudaError_t e = cudaFuncGetAttributes(&at, reinterpret_cast<const void*>(fp8_gemm_pair_kernel));
+  if (e != cudaSuccess) return e;
+  if (at.numRegs != FP_REGS) return cudaErrorInvalidConfiguration;
+  e = allow_smem(reinterpret_cast<const void*>(fp8_gemm_pair_kernel));
+  if (e != cudaSuccess) return e;
+  const long long most = sm_count() / 2;
+  return launch_pdl(fp8_gemm_pair_kernel, dim3((unsigned)(2 * (tiles < most ? tiles : most))),
+                    dim3(FP_THREADS), fp_smem(a.G), st, a, mp);
 }
 
 }  // namespace
 
-// Narrower tiles while there are fewer of them than SMs: a tile's time is then
-// the latency of its own chain of blocks, and more SMs share the weight stream.
+// The tile width with the least estimated time.  A wave of tiles costs the
+// bytes that a block loads per k-block, the rows of A and of W, since that is
+// what bounds it (the L2's rate for wide tiles, HBM's for narrow ones), plus a
+// fixed part.
 cudaError_t launch_fp8_gemm(const GemmArgs& a, cudaStream_t st) {
   // row tiles: the groups hold M rows in all, each at most one partial tile
-  const long long mt = a.offsets ? a.M / FG_BM + (a.G < a.M ? a.G : a.M)
-                                 : (a.M + FG_BM - 1) / FG_BM;
+  const int groups = a.offsets ? (a.G < a.M ? a.G : a.M) : 1;
+  auto row_tiles = [&](int bm) -> long long {
+    return a.offsets ? a.M / bm + groups : (a.M + bm - 1) / bm;
+  };
+  const long long avg = (a.M + groups - 1) / groups;
+  const long long rows = avg >= FG_BM ? FG_BM : (avg + 31) / 32 * 32;
+  const bool few = a.M <= 32;      // no tile has more than 32 rows
   const int sms = sm_count();
-  auto tiles = [&](int bn) { return mt * ((a.N + bn - 1) / bn); };
-  if (tiles(256) >= sms) return fg_launch<256>(a, tiles(256), st);
-  if (tiles(128) >= sms) return fg_launch<128>(a, tiles(128), st);
-  if (tiles(64) >= sms) return fg_launch<64>(a, tiles(64), st);
-  if (tiles(32) >= sms) return fg_launch<32>(a, tiles(32), st);
-  return fg_launch<16>(a, tiles(16), st);
+  long long best = 0, tiles = 0;
+  int bn = 0;
+  for (int b = 128; b >= 16; b >>= 1) {
+    const long long t = row_tiles(FG_BM) * ((a.N + b - 1) / b);
+    const long long cost = (t + sms - 1) / sms * (rows + b + 32);
+    if (bn == 0 || cost < best) {
+      best = cost;
+      bn = b;
+      tiles = t;
+    }
+  }
+  if (avg > FG_BM) {
+    const long long t = row_tiles(2 * FG_BM) * ((a.N + 255) / 256);
+    const long long cost = (t + sms / 2 - 1) / (sms / 2) * (FG_BM + FG_BM + 32);
+    if (cost < best) return fg_launch_pair(a, t, st);
+  }
+  if (few) {
+    switch (bn) {
+      case 128: return fg_launch<128, 32>(a, tiles, st);
+      case 64: return fg_launch<64, 32>(a, tiles, st);
+      case 32: return fg_launch<32, 32>(a, tiles, st);
+      default: return fg_launch<16, 32>(a, tiles, st);
+    }
+  }
+  switch (bn) {
+    case 128: return fg_launch<128, 128>(a, tiles, st);
+    case 64: return fg_launch<64, 128>(a, tiles, st);
+    case 32: return fg_launch<32, 128>(a, tiles, st);
+    default: return fg_launch<16, 128>(a, tiles, st);
+  }
 }
 
 }  // namespace moe

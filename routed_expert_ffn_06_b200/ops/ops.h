@@ -14,6 +14,9 @@ constexpr float kE4m3Max = 448.f;
 
 __host__ __device__ inline int blocks128(int n) { return (n + kBlock128 - 1) / kBlock128; }
 
+// Let a kernel use all of the shared memory a block may have (227 KB).
+cudaError_t allow_smem(const void* kernel);
+
 struct NormArgs {
   int d, T;
   int gate_kind;

@@ -100,6 +100,11 @@ Fp8LayerDev to_dev(const moe_fp8_layer* l) {
 }
 
 }  // namespace
+
+cudaError_t allow_smem(const void* kernel) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+}
+
 }  // namespace moe
 
 using namespace moe;
