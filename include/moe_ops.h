@@ -170,9 +170,11 @@ size_t moe_fp8_layer_workspace_bytes(const moe_fp8_layer* layer, int32_t max_tok
  *   to the lower expert index, NaN below every number)
  *   y = FFN_shared(x) + sum_j w[j] * FFN_{ids[j]}(x)  -> bf16
  * with FFN as in moe.h and each weight = code * its block's scale.  Activations
- * stay bf16 (they are not quantised) and the hidden values, with the routing
- * weight folded in, are kept to 16 mantissa bits (two bf16 terms); sums are
- * fp32.  Weight codes 0x7F and 0xFF read as +-480, not NaN.
+ * are not quantised: a token's columns enter the gate/up products exactly, except
+ * that in each 128 columns values below 2^-13 of the largest are off by up to
+ * 2^-21 of it; the hidden values, with the routing weight folded in, enter the
+ * down product in fp16 after a power-of-two scale per expert and token.  Sums
+ * are fp32.  An infinity or NaN in a token makes its row of y NaN.
  *  x: dev bf16 [T][d]; y: dev bf16 [T][d], not x; both 16-byte aligned.
  *  ids_or_null: dev int32 [T][k]; w_or_null: dev fp32 [T][k]: the routing,
  *  written when non-NULL.

@@ -24,6 +24,7 @@
 #include <cudaTypedefs.h>
 
 #include "ops.h"
+#include "pipe.cuh"
 #include "tc.cuh"
 
 namespace moe {
@@ -89,38 +90,6 @@ __device__ __forceinline__ void fg_mma(uint32_t d_tmem, uint64_t adesc, uint64_t
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
-}
-
-// A wait of the running pipeline.  The warps that wait stay whole without
-// voting on the outcome (a vote costs about 60 cycles, as much as the wait
-// itself): a wait that runs out (moe.h's limit; the timer is only read after
-// kPolls polls) records the error and raises the block's `gave_up` flag, and from
-// then on every wait of the block returns at once.  The roles then run to
-// their ends on whatever the memory holds; the outputs are undefined, no copy or
-// MMA outlives the block (fg_drain).
-constexpr int kPolls = 4096;
-__device__ __forceinline__ void fg_wait(uint64_t* bar, uint32_t parity, Control* ctl,
-                                        uint32_t where, uint32_t* gave_up) {
-  if (mbar_try_wait(bar, parity)) return;
-  for (int i = 1;; ++i) {
-    if (mbar_try_wait(bar, parity)) return;
-    if ((i & 63) == 0) {
-      if (*reinterpret_cast<volatile uint32_t*>(gave_up)) return;
-      if (i >= kPolls) {
-        if (!mbar_wait(bar, parity, ctl, where)) *reinterpret_cast<volatile uint32_t*>(gave_up) = 1u;
-        return;
-      }
-    }
-  }
-}
-
-// Copies in flight when a block gave up may count on barriers that it can no
-// longer follow: it outlives them by time.
-__device__ __forceinline__ void fg_drain(const uint32_t* gave_up) {
-  if (*reinterpret_cast<const volatile uint32_t*>(gave_up)) {
-    const unsigned long long t0 = globaltimer_ns();
-    while (globaltimer_ns() - t0 < kWaitFloorNs) __nanosleep(1000);
-  }
 }
 
 template <int N>
@@ -383,7 +352,7 @@ __global__ void __launch_bounds__(FG_THREADS, 1) fp8_gemm_kernel(
       const uint32_t bytes = ((pieces ? pieces * 32 : FG_BM) + BN) * FG_BK;
       for (int kb = 0; kb < KB; kb += KBS) {
         if (fills == C::kStages) {
-          fg_wait(&empty[s], ph ^ 1u, a.ctl, 0x401, gave_up);
+          pipe_wait(&empty[s], ph ^ 1u, a.ctl, 0x401, gave_up);
         } else {
           ++fills;
         }
@@ -414,8 +383,8 @@ __global__ void __launch_bounds__(FG_THREADS, 1) fp8_gemm_kernel(
     }
     // the newest phase of each stage may be unconsumed: its copies land first
     for (long long j = n - fills; j < n; ++j)
-      fg_wait(&full[j % C::kStages], (uint32_t)(j / C::kStages) & 1u, a.ctl, 0x402, gave_up);
-    fg_drain(gave_up);
+      pipe_wait(&full[j % C::kStages], (uint32_t)(j / C::kStages) & 1u, a.ctl, 0x402, gave_up);
+    pipe_drain(gave_up);
   } else if (warp == 1) {
     // kind::f8f6f4: e4m3 A and B (format 0), fp32 D, both K-major
     const uint32_t idesc = idesc_f16_f32(FG_BM, BN);
@@ -427,11 +396,11 @@ __global__ void __launch_bounds__(FG_THREADS, 1) fp8_gemm_kernel(
          t += gridDim.x) {
       for (int kb = 0; kb < KB; kb += KBS) {
         if (used == C::kGroups) {
-          fg_wait(&acce[as], aph ^ 1u, a.ctl, 0x403, gave_up);
+          pipe_wait(&acce[as], aph ^ 1u, a.ctl, 0x403, gave_up);
         } else {
           ++used;
         }
-        fg_wait(&full[s], ph, a.ctl, 0x404, gave_up);
+        pipe_wait(&full[s], ph, a.ctl, 0x404, gave_up);
         tc_fence_after();
         if (elected) {
           const uint64_t st = desc0 + (uint64_t)(s * (C::kStage >> 4));
@@ -498,7 +467,7 @@ __global__ void __launch_bounds__(FG_THREADS, 1) fp8_gemm_kernel(
           sa_n[j] = more ? sa[kb + KBS + j] : 0.f;
           sw_n[j] = more ? sw[kb + KBS + j] : 0.f;
         }
-        fg_wait(&accf[as], aph, a.ctl, 0x406, gave_up);
+        pipe_wait(&accf[as], aph, a.ctl, 0x406, gave_up);
         if (!idle) {
           tc_fence_after();
           const uint32_t base = lane_base + (uint32_t)(as * KBS * BN);
@@ -681,7 +650,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP_THREADS, 1)
         const int arow = tl.m0 + rank * FG_BM, wrow = tl.g * a.N + tl.n0 + rank * 64;
         for (int kb = 0; kb < KB; ++kb) {
           if (fills == FP_STAGES) {
-            fg_wait(&empty[s], ph ^ 1u, a.ctl, 0x411, gave_up);
+            pipe_wait(&empty[s], ph ^ 1u, a.ctl, 0x411, gave_up);
           } else {
             ++fills;
           }
@@ -710,8 +679,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP_THREADS, 1)
       // blocks land before either block ends (the cluster barrier below)
       if (rank == 0)
         for (long long j = n - fills; j < n; ++j)
-          fg_wait(&full[j % FP_STAGES], (uint32_t)(j / FP_STAGES) & 1u, a.ctl, 0x412, gave_up);
-      fg_drain(gave_up);
+          pipe_wait(&full[j % FP_STAGES], (uint32_t)(j / FP_STAGES) & 1u, a.ctl, 0x412, gave_up);
+      pipe_drain(gave_up);
     } else if (warp == 1 && rank == 0) {
       const uint32_t idesc = idesc_f16_f32(BM, BN / 2);
       const uint64_t desc0 = sw128_kmajor_desc(smem_u32(smem));
@@ -720,12 +689,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP_THREADS, 1)
       FgTile tl;
       for (long long t = pair; fg_tile(t, a, BM, BN, rows, first, &tl); t += pairs) {
         for (int kb = 0; kb < KB; ++kb) {
-          fg_wait(&full[s], ph, a.ctl, 0x414, gave_up);
+          pipe_wait(&full[s], ph, a.ctl, 0x414, gave_up);
           const uint64_t ad = desc0 + (uint64_t)(s * (FP_STAGE >> 4)), bd = ad + (FP_HALF >> 4);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             if (used == FP_SLOTS) {
-              fg_wait(&acce[as], aph ^ 1u, a.ctl, 0x413, gave_up);
+              pipe_wait(&acce[as], aph ^ 1u, a.ctl, 0x413, gave_up);
             } else {
               ++used;
             }
@@ -781,7 +750,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP_THREADS, 1)
           sa_n = sa[kb + 1];
           sw_n = sw[kb + 1];
         }
-        fg_wait(&accf[2 * as + part], aph, a.ctl, 0x416, gave_up);
+        pipe_wait(&accf[2 * as + part], aph, a.ctl, 0x416, gave_up);
         if (!idle) {
           tc_fence_after();
           const uint32_t base = lane_base + (uint32_t)(as * BN);
@@ -892,7 +861,8 @@ cudaError_t fg_launch(const GemmArgs& a, long long tiles, cudaStream_t st) {
       !fg_map(&mp.a32, a.a, (uint64_t)a.K, (uint64_t)a.M, 32) ||
       !fg_map(&mp.w, a.w, (uint64_t)a.K, (uint64_t)a.N * a.G, BN))
     return cudaErrorInvalidValue;
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(fp8_gemm_kernel<BN, AR>));
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(fp8_gemm_kernel<BN, AR>),
+                                   FgCfg<BN, AR>::smem(a.G));
   if (e != cudaSuccess) return e;
   const long long grid = tiles < sm_count() ? tiles : sm_count();
   return launch_pdl(fp8_gemm_kernel<BN, AR>, dim3((unsigned)grid), dim3(FG_THREADS),
@@ -919,7 +889,7 @@ cudaError_t fg_launch_pair(const GemmArgs& a, long long tiles, cudaStream_t st) 
   cudaError_t e = cudaFuncGetAttributes(&at, reinterpret_cast<const void*>(fp8_gemm_pair_kernel));
   if (e != cudaSuccess) return e;
   if (at.numRegs != FP_REGS) return cudaErrorInvalidConfiguration;
-  e = allow_smem(reinterpret_cast<const void*>(fp8_gemm_pair_kernel));
+  e = allow_smem(reinterpret_cast<const void*>(fp8_gemm_pair_kernel), fp_smem(a.G));
   if (e != cudaSuccess) return e;
   const long long most = sm_count() / 2;
   return launch_pdl(fp8_gemm_pair_kernel, dim3((unsigned)(2 * (tiles < most ? tiles : most))),

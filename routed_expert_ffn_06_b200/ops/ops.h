@@ -14,8 +14,8 @@ constexpr float kE4m3Max = 448.f;
 
 __host__ __device__ inline int blocks128(int n) { return (n + kBlock128 - 1) / kBlock128; }
 
-// Let a kernel use all of the shared memory a block may have (227 KB).
-cudaError_t allow_smem(const void* kernel);
+// Let a kernel use that much dynamic shared memory.
+cudaError_t allow_smem(const void* kernel, size_t bytes);
 
 struct NormArgs {
   int d, T;

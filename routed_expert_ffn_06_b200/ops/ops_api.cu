@@ -101,8 +101,8 @@ Fp8LayerDev to_dev(const moe_fp8_layer* l) {
 
 }  // namespace
 
-cudaError_t allow_smem(const void* kernel) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+cudaError_t allow_smem(const void* kernel, size_t bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
 }  // namespace moe
