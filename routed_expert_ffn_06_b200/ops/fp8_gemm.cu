@@ -69,7 +69,7 @@ struct FgCfg {
 
 // A by tiles of 128 rows, and by pieces of 32 rows for tiles with few.
 struct alignas(64) FgMaps {
-  CUtensorMap a, a32, w, c;     // c: output by 32 rows x 64 columns (pairs of blocks only)
+  CUtensorMap a, a32, w, c;     // c: output by 32 rows x 64 columns (wide tiles only)
 };
 
 __device__ __forceinline__ void fg_tma_2d(void* dst, const CUtensorMap* map, int c0, int c1,
@@ -510,114 +510,67 @@ __global__ void __launch_bounds__(FG_THREADS, 1) fp8_gemm_kernel(
   if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
 }
 
-// ------------------------------------------------------- two SMs on one tile
-// 256 x 256 tiles for many rows: a pair of blocks shares one tcgen05.mma
-// (cta_group::2, M = 256). Each block loads its own 128 rows of A and half of
-// the tile's W, 32 KB per k-block instead of the 48 KB a block of its own would
-// load for the same work: the L2 delivers about 68 bytes per cycle and SM
-// (measured), so 48 KB take 720 cycles and 32 KB take 480, less than the 540 of
-// the MMAs themselves. Both loaders count their bytes on the even block's
-// barriers; the even block's commits release both blocks.
+// ------------------------------------------------------------ wide tiles
+// 128 x 256 tiles for many rows.  The L2 delivers about 68 bytes per cycle and SM
+// (measured), so a k-block's 48 KB take 720 cycles, against 540 of the MMAs; 128 x
+// 128 tiles would need 480 cycles for 270.  (Pairs of SMs on 256 x 256 tiles load
+// 32 KB per SM and k-block, but the hand-overs between two SMs cost more than that
+// saves: 65 us for 8192 x 4096 x 2048, with the same four accumulators.)
 //
-// A hand-over between roles of two SMs takes some hundred cycles, so a k-block
-// is two MMA groups of 128 columns, each with two TMEM accumulators and four
-// epilogue warps of its own: while one accumulator of a half is read back, its
-// other one and the other half keep the tensor cores busy.  Eight epilogue warps
-// per block hold 128 sums a thread, with the registers that the other warps
-// give up (setmaxnreg).
-constexpr int FP_STAGES = 4;
-constexpr int FP_HALF = FG_BM * FG_BK;                 // 16 KB: 128 rows of a k-block
-constexpr int FP_STAGE = 2 * FP_HALF;
-constexpr int FP_THREADS = 384;                        // 4 warps of roles, 8 of epilogue
-constexpr int FP_SLOTS = 4;                            // TMEM accumulators of 128 columns
-constexpr int FP_OUT_BYTES = FG_EPI_WARPS * 32 * 128 * 2;   // a warp's 32 rows x 128 columns
-constexpr int FP_REGS = 168, FP_REGS_ROLE = 40, FP_REGS_EPI = 232;
-static_assert(4 * FP_REGS_ROLE + 8 * FP_REGS_EPI <= 12 * FP_REGS,
+// One tcgen05.mma takes all 256 columns: at 128 columns a block's MMAs read A
+// twice and shared memory at 122 bytes per cycle, which nearly halves their rate.
+// TMEM holds two accumulators; two epilogue warps per lane quarter hold 128 sums a
+// thread, with the registers that the other warps give up (setmaxnreg).
+constexpr int FW_HALF = FG_BM * FG_BK;                 // 16 KB: 128 rows of a k-block
+constexpr int FW_STAGE = 3 * FW_HALF;                  // A, two halves of W
+constexpr int FW_MAX_STAGES = 4;
+constexpr int FW_THREADS = 384;                        // 4 warps of roles, 8 of epilogue
+constexpr int FW_SLOTS = 2;                            // TMEM accumulators of 256 columns
+constexpr int FW_OUT = 32 * 64 * 2;                    // staging of a warp: 32 rows x 64 columns
+constexpr int FW_REGS = 168, FW_REGS_ROLE = 40, FW_REGS_EPI = 232;
+static_assert(4 * FW_REGS_ROLE + 8 * FW_REGS_EPI <= 12 * FW_REGS,
               "setmaxnreg hands out what the block was launched with");
 
-__host__ __device__ constexpr size_t fp_smem(int G) {
-  return 1024 + (size_t)FP_STAGES * FP_STAGE + FP_OUT_BYTES + (2 * FP_STAGES + 2 * FP_SLOTS + 1) * 8 + 16 +
-         (size_t)(2 * G + 2) * 4;
+__host__ __device__ constexpr size_t fw_smem(int stages, int G) {
+  return 1024 + (size_t)stages * FW_STAGE + FG_EPI_WARPS * FW_OUT +
+         (2 * FW_MAX_STAGES + 2 * FW_SLOTS + 1) * 8 + 16 + (size_t)(2 * G + 2) * 4;
 }
 
-__device__ __forceinline__ uint32_t fp_even(const void* p) {   // p's place in the even block
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
-  return r;
-}
-__device__ __forceinline__ void fp_cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                   : "memory");
-}
-// A load whose bytes count on a barrier of the pair's even block.
-__device__ __forceinline__ void fp_tma_2d(void* dst, const CUtensorMap* map, int c0, int c1,
-                                          uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void fp_mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
-                                       uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// Arrive on the barrier at this place of both blocks once the MMAs issued so
-// far have completed.
-__device__ __forceinline__ void fp_commit(uint64_t* bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
-      "[%0], %1;" ::"r"(smem_u32(bar)),
-      "h"((uint16_t)3)
-      : "memory");
-}
-__device__ __forceinline__ void fp_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP_THREADS, 1)
-    fp8_gemm_pair_kernel(GemmArgs a, const __grid_constant__ FgMaps mp) {
-  constexpr int BM = 256, BN = 256;
+__global__ void __launch_bounds__(FW_THREADS, 1)
+    fp8_gemm_wide_kernel(GemmArgs a, int stages, const __grid_constant__ FgMaps mp) {
+  constexpr int BN = 256;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  unsigned char* out_s = smem + FP_STAGES * FP_STAGE;
-  uint64_t* full = reinterpret_cast<uint64_t*>(out_s + FP_OUT_BYTES);
-  uint64_t* empty = full + FP_STAGES;
-  uint64_t* accf = empty + FP_STAGES;
-  uint64_t* acce = accf + FP_SLOTS;
-  uint64_t* done = acce + FP_SLOTS;
+  unsigned char* out_s = smem + stages * FW_STAGE;
+  uint64_t* full = reinterpret_cast<uint64_t*>(out_s + FG_EPI_WARPS * FW_OUT);
+  uint64_t* empty = full + FW_MAX_STAGES;
+  uint64_t* accf = empty + FW_MAX_STAGES;
+  uint64_t* acce = accf + FW_SLOTS;
+  uint64_t* done = acce + FW_SLOTS;
   uint32_t* holder = reinterpret_cast<uint32_t*>(done + 1);
   uint32_t* gave_up = holder + 1;
   int* rows = reinterpret_cast<int*>(holder + 4);
   int* first = rows + a.G + 1;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int KB = blocks128(a.K);
 
   if (tid == 0) {
-    for (int s = 0; s < FP_STAGES; ++s) {
+    for (int s = 0; s < stages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int s = 0; s < FP_SLOTS; ++s) {
+    for (int s = 0; s < FW_SLOTS; ++s) {
       mbar_init(&accf[s], 1);
-      mbar_init(&acce[s], FG_EPI_WARPS);      // four warps of each block
+      mbar_init(&acce[s], FG_EPI_WARPS);
     }
     mbar_init(done, 1);
     *gave_up = 0u;
     fence_barrier_init();
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
-                     smem_u32(holder))
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    tmem_alloc(holder, 512);
+    tmem_relinquish();
   }
   if (warp == 0 && lane < 3)
     asm volatile("prefetch.tensormap [%0];" ::"l"(
@@ -625,116 +578,100 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP_THREADS, 1)
                  : "memory");
   pdl_wait();
   pdl_launch_dependents();
-  fg_groups(a, rows, first, BM);
+  fg_groups(a, rows, first);
   tc_fence_before();
   __syncthreads();
-  fp_cluster_sync();       // both blocks' barriers are initialised
   tc_fence_after();
   const uint32_t tmem = *holder;
   const bool elected = elect_one();
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FP_REGS_ROLE));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FW_REGS_ROLE));
     if (warp == 0) {
       int s = 0;
       uint32_t ph = 0;
       int fills = 0;
       long long n = 0;
       FgTile tl;
-      for (long long t = pair; fg_tile(t, a, BM, BN, rows, first, &tl); t += pairs) {
-        // valid rows of each block's half, loaded by pieces of 32 where few
-        const int r0 = min(FG_BM, tl.m_end - tl.m0), r1 = max(0, min(FG_BM, tl.m_end - tl.m0 - FG_BM));
-        const int p0 = r0 > 96 ? 4 : (r0 + 31) / 32, p1 = r1 > 96 ? 4 : (r1 + 31) / 32;
-        const int mine = rank ? p1 : p0;
-        const uint32_t bytes = (uint32_t)(p0 + p1) * 32 * FG_BK + 2 * FP_HALF;
-        const int arow = tl.m0 + rank * FG_BM, wrow = tl.g * a.N + tl.n0 + rank * 64;
+      for (long long t = blockIdx.x; fg_tile(t, a, FG_BM, BN, rows, first, &tl); t += gridDim.x) {
+        const int nrow = min(FG_BM, tl.m_end - tl.m0), pieces = nrow > 96 ? 0 : (nrow + 31) / 32;
+        const uint32_t bytes = ((pieces ? pieces * 32 : FG_BM) + BN) * FG_BK;
+        const int wrow = tl.g * a.N + tl.n0;
         for (int kb = 0; kb < KB; ++kb) {
-          if (fills == FP_STAGES) {
+          if (fills == stages) {
             pipe_wait(&empty[s], ph ^ 1u, a.ctl, 0x411, gave_up);
           } else {
             ++fills;
           }
           if (elected) {
-            unsigned char* st = smem + s * FP_STAGE;
-            const uint32_t bar = fp_even(&full[s]);
-            if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
-            if (mine == 4) {
-              fp_tma_2d(st, &mp.a, kb * FG_BK, arow, bar);
+            unsigned char* st = smem + s * FW_STAGE;
+            mbar_arrive_expect_tx(&full[s], bytes);
+            if (pieces == 0) {
+              fg_tma_2d(st, &mp.a, kb * FG_BK, tl.m0, &full[s]);
             } else {
-              for (int p = 0; p < mine; ++p)
-                fp_tma_2d(st + p * 32 * FG_BK, &mp.a32, kb * FG_BK, arow + 32 * p, bar);
+              for (int p = 0; p < pieces; ++p)
+                fg_tma_2d(st + p * 32 * FG_BK, &mp.a32, kb * FG_BK, tl.m0 + 32 * p, &full[s]);
             }
-            // half h of the columns: 64 rows of W in each block
-            fp_tma_2d(st + FP_HALF, &mp.w, kb * FG_BK, wrow, bar);
-            fp_tma_2d(st + FP_HALF + FP_HALF / 2, &mp.w, kb * FG_BK, wrow + 128, bar);
+            fg_tma_2d(st + FW_HALF, &mp.w, kb * FG_BK, wrow, &full[s]);
           }
           ++n;
-          if (++s == FP_STAGES) {
+          if (++s == stages) {
             s = 0;
             ph ^= 1u;
           }
         }
       }
-      // the newest phase of each stage may be unconsumed: the copies of both
-      // blocks land before either block ends (the cluster barrier below)
-      if (rank == 0)
-        for (long long j = n - fills; j < n; ++j)
-          pipe_wait(&full[j % FP_STAGES], (uint32_t)(j / FP_STAGES) & 1u, a.ctl, 0x412, gave_up);
+      // the newest phase of each stage may be unconsumed: its copies land first
+      for (long long j = n - fills; j < n; ++j)
+        pipe_wait(&full[j % stages], (uint32_t)(j / stages) & 1u, a.ctl, 0x412, gave_up);
       pipe_drain(gave_up);
-    } else if (warp == 1 && rank == 0) {
-      const uint32_t idesc = idesc_f16_f32(BM, BN / 2);
+    } else if (warp == 1) {
+      const uint32_t idesc = idesc_f16_f32(FG_BM, BN);
       const uint64_t desc0 = sw128_kmajor_desc(smem_u32(smem));
       int s = 0, as = 0, used = 0;
       uint32_t ph = 0, aph = 0;
       FgTile tl;
-      for (long long t = pair; fg_tile(t, a, BM, BN, rows, first, &tl); t += pairs) {
+      for (long long t = blockIdx.x; fg_tile(t, a, FG_BM, BN, rows, first, &tl); t += gridDim.x) {
         for (int kb = 0; kb < KB; ++kb) {
           pipe_wait(&full[s], ph, a.ctl, 0x414, gave_up);
-          const uint64_t ad = desc0 + (uint64_t)(s * (FP_STAGE >> 4)), bd = ad + (FP_HALF >> 4);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (used == FP_SLOTS) {
-              pipe_wait(&acce[as], aph ^ 1u, a.ctl, 0x413, gave_up);
-            } else {
-              ++used;
-            }
-            tc_fence_after();
-            if (elected) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                fp_mma(tmem + (uint32_t)(as * (BN / 2)), ad + 2 * i, bd + 2 * i + h * (FP_HALF >> 5),
-                       idesc, i > 0 ? 1u : 0u);
-              fp_commit(&accf[as]);
-              if (h == 1) fp_commit(&empty[s]);
-            }
-            if (++as == FP_SLOTS) {
-              as = 0;
-              aph ^= 1u;
-            }
+          if (used == FW_SLOTS) {
+            pipe_wait(&acce[as], aph ^ 1u, a.ctl, 0x413, gave_up);
+          } else {
+            ++used;
           }
-          if (++s == FP_STAGES) {
+          tc_fence_after();
+          if (elected) {
+            const uint64_t ad = desc0 + (uint64_t)(s * (FW_STAGE >> 4)), bd = ad + (FW_HALF >> 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              fg_mma(tmem + (uint32_t)(as * BN), ad + 2 * i, bd + 2 * i, idesc, i > 0 ? 1u : 0u);
+            tc_commit(&accf[as]);
+            tc_commit(&empty[s]);
+          }
+          as ^= 1;
+          if (as == 0) aph ^= 1u;
+          if (++s == stages) {
             s = 0;
             ph ^= 1u;
           }
         }
       }
-      // every MMA issued has completed before the pair frees its TMEM
-      if (elected) fp_commit(done);
+      // every MMA issued has completed before this warp frees the TMEM
+      if (elected) tc_commit(done);
       mbar_wait(done, 0, a.ctl, 0x415);
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(FP_REGS_EPI));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(FW_REGS_EPI));
     constexpr int COLS = 128, LD = 32;
     const int ew = warp - 4, q = warp & 3, part = ew >> 2;     // part: the half of the columns
     const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(part * COLS);
-    unsigned char* stage = out_s + ew * (32 * COLS * 2);
-    const uint32_t free_bar = fp_even(&acce[part]);
+    unsigned char* stage = out_s + ew * FW_OUT;
     const bool tma_out = (a.N & 7) == 0 && (reinterpret_cast<uintptr_t>(a.c) & 15) == 0;
-    int as = 0;           // accumulator 2 * as + part
+    int as = 0;
     uint32_t aph = 0;
     FgTile tl;
-    for (long long t = pair; fg_tile(t, a, BM, BN, rows, first, &tl); t += pairs) {
-      const int row0 = tl.m0 + rank * FG_BM + 32 * q, row = row0 + lane;
+    for (long long t = blockIdx.x; fg_tile(t, a, FG_BM, BN, rows, first, &tl); t += gridDim.x) {
+      const int row0 = tl.m0 + 32 * q, row = row0 + lane;
       const int col0 = tl.n0 + part * COLS;
       const bool idle = row0 >= tl.m_end || col0 >= a.N;
       const float* sa = a.a_scales + (long long)min(row, a.M - 1) * KB;
@@ -750,7 +687,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP_THREADS, 1)
           sa_n = sa[kb + 1];
           sw_n = sw[kb + 1];
         }
-        pipe_wait(&accf[2 * as + part], aph, a.ctl, 0x416, gave_up);
+        pipe_wait(&accf[as], aph, a.ctl, 0x416, gave_up);
         if (!idle) {
           tc_fence_after();
           const uint32_t base = lane_base + (uint32_t)(as * BN);
@@ -765,7 +702,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP_THREADS, 1)
             } else {
               // everything is in registers: hand the accumulator back before the last sums
               tc_fence_before();
-              if (elected) fp_arrive(free_bar + 16 * as);
+              if (elected) fg_arrive(&acce[as]);
             }
 #pragma unroll
             for (int x = 0; x < LD; x += 2)
@@ -773,48 +710,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP_THREADS, 1)
                    make_float2(__uint_as_float(v[i & 1][x]), __uint_as_float(v[i & 1][x + 1])), sc2);
           }
         } else if (elected) {
-          fp_arrive(free_bar + 16 * as);
+          fg_arrive(&acce[as]);
         }
         as ^= 1;
         if (as == 0) aph ^= 1u;
       }
       if (idle) continue;
-      // the staging buffer is free once the previous tile's store has read it
-      if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-      __syncwarp();
       if (tma_out && (!a.offsets || row0 + 32 <= tl.m_end)) {
-        // a TMA store of 32 rows x 64 columns twice (128-byte swizzle: piece p of
-        // row r at p ^ (r & 7)); the copy clips rows and columns of no product,
-        // and runs while the next tile is summed
+        // TMA stores of 32 rows x 64 columns (128-byte swizzle: piece p of row r at
+        // p ^ (r & 7)); the copy clips rows and columns of no product, and the
+        // second runs while the next tile is summed
 #pragma unroll
-        for (int p = 0; p < COLS / 8; ++p) {
-          uint32_t w[4];
+        for (int h = 0; h < 2; ++h) {
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          __syncwarp();
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 f = acc[4 * p + j];
-            const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
-            w[j] = *reinterpret_cast<const uint32_t*>(&b);
+          for (int p = 0; p < 8; ++p) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 f = acc[32 * h + 4 * p + j];
+              const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
+              w[j] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+            *reinterpret_cast<uint4*>(stage + lane * 128 + ((p ^ (lane & 7)) << 4)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
           }
-          *reinterpret_cast<uint4*>(stage + (p >> 3) * 4096 + lane * 128 +
-                                    (((p & 7) ^ (lane & 7)) << 4)) =
-              make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            if (col0 + 64 * h < a.N)
-              asm volatile(
-                  "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
-                      reinterpret_cast<uint64_t>(&mp.c)),
-                  "r"(col0 + 64 * h), "r"(row0), "r"(smem_u32(stage + h * 4096))
-                  : "memory");
-          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && col0 + 64 * h < a.N) {
+            asm volatile(
+                "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                    reinterpret_cast<uint64_t>(&mp.c)),
+                "r"(col0 + 64 * h), "r"(row0), "r"(smem_u32(stage))
+                : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
         }
       } else {
+        // the staging buffer is free once the previous tile's store has read it
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        __syncwarp();
         fg_store<COLS, 64>(a, acc, reinterpret_cast<uint32_t*>(stage), row0,
                            min(32, tl.m_end - row0), col0, lane);
+        __syncwarp();
       }
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -822,10 +761,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP_THREADS, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  fp_cluster_sync();       // no block ends while the other may still use its memory
   tc_fence_after();
-  if (warp == 1)
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 fg_encode() {
@@ -869,11 +806,11 @@ cudaError_t fg_launch(const GemmArgs& a, long long tiles, cudaStream_t st) {
                     FgCfg<BN, AR>::smem(a.G), st, a, mp);
 }
 
-cudaError_t fg_launch_pair(const GemmArgs& a, long long tiles, cudaStream_t st) {
+cudaError_t fg_launch_wide(const GemmArgs& a, long long tiles, cudaStream_t st) {
   FgMaps mp = {};
   if (!fg_map(&mp.a, a.a, (uint64_t)a.K, (uint64_t)a.M, FG_BM) ||
       !fg_map(&mp.a32, a.a, (uint64_t)a.K, (uint64_t)a.M, 32) ||
-      !fg_map(&mp.w, a.w, (uint64_t)a.K, (uint64_t)a.N * a.G, 64))
+      !fg_map(&mp.w, a.w, (uint64_t)a.K, (uint64_t)a.N * a.G, 256))
     return cudaErrorInvalidValue;
   if ((a.N & 7) == 0 && (reinterpret_cast<uintptr_t>(a.c) & 15) == 0) {
     cuuint64_t dims[2] = {(cuuint64_t)a.N, (cuuint64_t)a.M}, strides[1] = {(cuuint64_t)a.N * 2};
@@ -886,14 +823,17 @@ cudaError_t fg_launch_pair(const GemmArgs& a, long long tiles, cudaStream_t st) 
   }
   // a block launched with fewer registers than the split hands out would wait for ever
   cudaFuncAttributes at;
-  cudaError_t e = cudaFuncGetAttributes(&at, reinterpret_cast<const void*>(fp8_gemm_pair_kernel));
+  cudaError_t e = cudaFuncGetAttributes(&at, reinterpret_cast<const void*>(fp8_gemm_wide_kernel));
   if (e != cudaSuccess) return e;
-  if (at.numRegs != FP_REGS) return cudaErrorInvalidConfiguration;
-  e = allow_smem(reinterpret_cast<const void*>(fp8_gemm_pair_kernel), fp_smem(a.G));
+  if (at.numRegs != FW_REGS) return cudaErrorInvalidConfiguration;
+  // the offsets of very many groups take the place of one stage
+  const int stages = fw_smem(FW_MAX_STAGES, a.G) <= 227 * 1024 ? FW_MAX_STAGES : FW_MAX_STAGES - 1;
+  const size_t sm = fw_smem(stages, a.G);
+  e = allow_smem(reinterpret_cast<const void*>(fp8_gemm_wide_kernel), sm);
   if (e != cudaSuccess) return e;
-  const long long most = sm_count() / 2;
-  return launch_pdl(fp8_gemm_pair_kernel, dim3((unsigned)(2 * (tiles < most ? tiles : most))),
-                    dim3(FP_THREADS), fp_smem(a.G), st, a, mp);
+  const long long grid = tiles < sm_count() ? tiles : sm_count();
+  return launch_pdl(fp8_gemm_wide_kernel, dim3((unsigned)grid), dim3(FW_THREADS), sm, st, a, stages,
+                    mp);
 }
 
 }  // namespace
@@ -923,10 +863,10 @@ cudaError_t launch_fp8_gemm(const GemmArgs& a, cudaStream_t st) {
       tiles = t;
     }
   }
-  if (avg > FG_BM) {
-    const long long t = row_tiles(2 * FG_BM) * ((a.N + 255) / 256);
-    const long long cost = (t + sms / 2 - 1) / (sms / 2) * (FG_BM + FG_BM + 32);
-    if (cost < best) return fg_launch_pair(a, t, st);
+  if (!few) {
+    const long long t = row_tiles(FG_BM) * ((a.N + 255) / 256);
+    const long long cost = (t + sms - 1) / sms * (rows + 256 + 32);
+    if (cost < best) return fg_launch_wide(a, t, st);
   }
   if (few) {
     switch (bn) {
