@@ -10,8 +10,12 @@
 // stores, so every byte is read once and written once; the kernel is bound by
 // HBM for many rows and by its launch and two dependent reductions for one.
 // A thread owns chunks of 8 consecutive channels (16-byte accesses in bf16).
-// Rows of up to 1024 channels take one warp each (no block barrier); wider
-// rows take a block each.  128 channels are 16 chunks = 16 consecutive lanes,
+// Rows of up to 512 channels take one warp each (no block barrier); wider rows
+// take a block each, of as many threads as chunks (measured: 777 x 1000 channels
+// 3.9 us against 6.6 us with a warp per row, 8192 x 1024 18.1 against 22.6; at
+// 30,000 x 512 the warps win, 22.8 against 32.4).  Blocks
+// that walk the rows, with the weights in registers and the next row on its way,
+// gained 2% at 8192 x 2048 and lost 20% at 8192 x 1024.  128 channels are 16 chunks = 16 consecutive lanes,
 // so the largest |h| of a scale block is a half-warp maximum.
 #include "ops.h"
 
@@ -62,11 +66,17 @@ __device__ __forceinline__ void quant8(const float (&v)[8], bool live, uint8_t* 
   if (!live) m = 0;
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float s = __fdiv_rn(__uint_as_float(m), kE4m3Max);
+  const float top = __uint_as_float(m), s = top * (1.f / kE4m3Max);
   if (!live) return;
+  // one division for the block; v / s would overflow it below about 1e-36
+  const float inv = kE4m3Max / fmaxf(top, 1e-30f);
   float q[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) q[j] = s != 0.f ? __fdiv_rn(v[j], s) : v[j];
+  for (int j = 0; j < 8; ++j) q[j] = v[j] * inv;
+  if (top < 1e-30f) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q[j] = s != 0.f ? v[j] / s : v[j];
+  }
   *reinterpret_cast<uint2*>(codes) =
       make_uint2(e4m3x4(q[0], q[1], q[2], q[3]), e4m3x4(q[4], q[5], q[6], q[7]));
   if ((threadIdx.x & 15) == 0) *scale = s;
@@ -83,6 +93,10 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
   __syncthreads();
   return warp_sum(lane < nw ? red[lane] : 0.f);
 }
+
+// 1 / (1 + e^-x): the fast exponential and reciprocal are off by |x| 2^-24 and a
+// few last bits, and exact division and exp took a third of the kernel's time.
+__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
 
 constexpr int kWarpRows = 4;   // rows (warps) of a block when a row takes one warp
 
@@ -124,7 +138,7 @@ __global__ void __launch_bounds__(WARP_ROW ? 32 * kWarpRows : 1024) norm_block_k
   float gt = 1.f;
   if (a.gate_kind == MOE_GATE_TOKEN) {
     gt = bf16_bits_to_float(a.gate[row]);
-    if (a.sigmoid) gt = 1.f / (1.f + expf(-gt));
+    if (a.sigmoid) gt = sigmoid(gt);
   }
   float inv_y = 1.f;
   if (a.post) {
@@ -136,7 +150,7 @@ __global__ void __launch_bounds__(WARP_ROW ? 32 * kWarpRows : 1024) norm_block_k
 #pragma unroll
       for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
     }
-    inv_y = rsqrtf(row_sum<WARP_ROW>(ss, red[0]) / (float)a.d + a.eps);
+    inv_y = rsqrtf(row_sum<WARP_ROW>(ss, red[0]) * a.inv_d + a.eps);
   }
   float ss = 0.f;
 #pragma unroll
@@ -157,7 +171,7 @@ __global__ void __launch_bounds__(WARP_ROW ? 32 * kWarpRows : 1024) norm_block_k
     if (a.gate_kind >= MOE_GATE_CHANNEL) {
       unpack8(gv[i], g);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) u[j] *= a.sigmoid ? 1.f / (1.f + expf(-g[j])) : g[j];
+      for (int j = 0; j < 8; ++j) u[j] *= a.sigmoid ? sigmoid(g[j]) : g[j];
     } else if (a.gate_kind == MOE_GATE_TOKEN) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) u[j] *= gt;
@@ -180,7 +194,7 @@ __global__ void __launch_bounds__(WARP_ROW ? 32 * kWarpRows : 1024) norm_block_k
     }
   }
   if (!a.h && !a.codes) return;
-  const float inv = rsqrtf(row_sum<WARP_ROW>(ss, red[1]) / (float)a.d + a.eps);
+  const float inv = rsqrtf(row_sum<WARP_ROW>(ss, red[1]) * a.inv_d + a.eps);
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = lane + i * nt;
@@ -234,7 +248,6 @@ cudaError_t launch_norm_t(const NormArgs& a, cudaStream_t st) {
   const int nc = a.d >> 3;
   if (nc <= 32) return launch_norm<F32, true, 1>(a, 32 * kWarpRows, st);
   if (nc <= 64) return launch_norm<F32, true, 2>(a, 32 * kWarpRows, st);
-  if (nc <= 128) return launch_norm<F32, true, 4>(a, 32 * kWarpRows, st);
   return launch_norm<F32, false, 1>(a, (nc + 31) / 32 * 32, st);
 }
 

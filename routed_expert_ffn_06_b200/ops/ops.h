@@ -22,6 +22,7 @@ struct NormArgs {
   int gate_kind;
   bool post, sigmoid;
   float eps, a, b;
+  float inv_d;                 // 1 / d
   float w_off;                 // added to the weights (1 when they are zero-centred)
   const float *pre_w, *post_w; // or nullptr
   long long x_ld, y_ld, gate_ld, x_out_ld, h_ld;

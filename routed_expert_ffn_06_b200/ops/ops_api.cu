@@ -152,6 +152,7 @@ moe_status moe_norm_block(const moe_norm* n, const void* x, const void* y_or_nul
   a.post = (n->flags & MOE_NORM_F_POST) && y_or_null;
   a.sigmoid = n->flags & MOE_NORM_F_SIGMOID;
   a.eps = n->eps;
+  a.inv_d = (float)(1.0 / n->d);
   a.a = n->stream_scale;
   a.b = n->branch_scale;
   a.w_off = (n->flags & MOE_NORM_F_ZERO_CENTRED) ? 1.f : 0.f;
