@@ -162,40 +162,45 @@ struct FgTile {
   int n0;        // first column
 };
 
-// Tiles run along the rows of one column stripe first inside a group, so that
-// neighbouring blocks share the weights of the stripe.
-__device__ __forceinline__ bool fg_tile(long long t, const GemmArgs& a, int bm, int bn,
-                                        const int* rows, const int* first, FgTile* o) {
+// The block's tile t, by a whole warp; o->g starts at 0 and goes along with t, which
+// only grows.  Tiles run along the rows of one column stripe first inside a group,
+// so that neighbouring blocks share the weights of the stripe.  The group is
+// looked for 32 at a time from the last one on (a binary search by each lane took
+// about 800 cycles, as long as two k-blocks).
+__device__ __forceinline__ bool fg_tile(long long t, const GemmArgs& a, int bn, const int* rows,
+                                        const int* first, FgTile* o) {
   const int nt = (a.N + bn - 1) / bn;
   if (t >= (long long)first[a.G] * nt) return false;
-  // the last group g with first[g] * nt <= t
-  int lo = 0, hi = a.G;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if ((long long)first[mid] * nt <= t) lo = mid; else hi = mid;
+  // the last group g with first[g] * nt <= t: empty groups share their start with
+  // the next one, so it is the one that holds tile t
+  int g = o->g;
+  if (a.G > 1) {
+    for (;;) {
+      const int i = g + 1 + (int)(threadIdx.x & 31);
+      const uint32_t m = __ballot_sync(0xffffffffu, i <= a.G && (long long)first[i] * nt <= t);
+      g += __popc(m);
+      if (m != 0xffffffffu) break;
+    }
   }
-  // empty groups share their start with the next one: lo is the last of them,
-  // and the only one that holds tiles
-  const int mt = first[lo + 1] - first[lo];
-  const int q = (int)(t - (long long)first[lo] * nt);
-  o->g = lo;
-  o->m0 = rows[lo] + (q % mt) * bm;
-  o->m_end = rows[lo + 1];
-  o->n0 = (q / mt) * bn;
+  const int mt = first[g + 1] - first[g];
+  const int q = (int)(t - (long long)first[g] * nt), n = q / mt;
+  o->g = g;
+  o->m0 = rows[g] + (q - n * mt) * FG_BM;
+  o->m_end = rows[g + 1];
+  o->n0 = n * bn;
   return true;
 }
 
-// Row range and row-tile count (tiles of bm rows) of each group, into shared
-// memory; the caller's barrier follows.
-__device__ __forceinline__ void fg_groups(const GemmArgs& a, int* rows, int* first,
-                                          int bm = FG_BM) {
+// Row range and row-tile count of each group, into shared memory; the caller's
+// barrier follows.
+__device__ __forceinline__ void fg_groups(const GemmArgs& a, int* rows, int* first) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (!a.offsets) {
     if (tid == 0) {
       rows[0] = 0;
       rows[1] = a.M;
       first[0] = 0;
-      first[1] = (a.M + bm - 1) / bm;
+      first[1] = (a.M + FG_BM - 1) / FG_BM;
     }
   } else if (warp == 0) {
     // one warp scans the offsets: a running maximum clamps them to 0..M and to
@@ -216,7 +221,7 @@ __device__ __forceinline__ void fg_groups(const GemmArgs& a, int* rows, int* fir
       int prev = __shfl_up_sync(0xffffffffu, v, 1);
       if (lane == 0) prev = top;
       // tiles of group g - 1 end at offset g
-      int n = (g >= 1 && g <= a.G) ? (v - prev + bm - 1) / bm : 0;
+      int n = (g >= 1 && g <= a.G) ? (v - prev + FG_BM - 1) / FG_BM : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int u = __shfl_up_sync(0xffffffffu, n, o);
@@ -343,8 +348,8 @@ __global__ void __launch_bounds__(FG_THREADS, 1) fp8_gemm_kernel(
     uint32_t ph = 0;
     int fills = 0;          // capped at kStages
     long long n = 0;
-    FgTile tl;
-    for (long long t = blockIdx.x; fg_tile(t, a, FG_BM, BN, rows, first, &tl);
+    FgTile tl = {};
+    for (long long t = blockIdx.x; fg_tile(t, a, BN, rows, first, &tl);
          t += gridDim.x) {
       const int wrow = tl.g * a.N + tl.n0;
       // Rows past the tile's last are not loaded, by pieces of 32.
@@ -391,8 +396,8 @@ __global__ void __launch_bounds__(FG_THREADS, 1) fp8_gemm_kernel(
     const uint64_t desc0 = sw128_kmajor_desc(smem_u32(smem));
     int s = 0, as = 0, used = 0;     // used: accumulator groups handed out, capped at kGroups
     uint32_t ph = 0, aph = 0;
-    FgTile tl;
-    for (long long t = blockIdx.x; fg_tile(t, a, FG_BM, BN, rows, first, &tl);
+    FgTile tl = {};
+    for (long long t = blockIdx.x; fg_tile(t, a, BN, rows, first, &tl);
          t += gridDim.x) {
       for (int kb = 0; kb < KB; kb += KBS) {
         if (used == C::kGroups) {
@@ -439,8 +444,8 @@ __global__ void __launch_bounds__(FG_THREADS, 1) fp8_gemm_kernel(
     constexpr int LD = C::kLd, CH = C::kCols / LD;     // loads per k-block
     int as = 0;
     uint32_t aph = 0;
-    FgTile tl;
-    for (long long t = blockIdx.x; fg_tile(t, a, FG_BM, BN, rows, first, &tl);
+    FgTile tl = {};
+    for (long long t = blockIdx.x; fg_tile(t, a, BN, rows, first, &tl);
          t += gridDim.x) {
       const int row0 = tl.m0 + 32 * q, row = row0 + lane;
       const int col0 = tl.n0 + part * C::kCols;
@@ -592,8 +597,8 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
       uint32_t ph = 0;
       int fills = 0;
       long long n = 0;
-      FgTile tl;
-      for (long long t = blockIdx.x; fg_tile(t, a, FG_BM, BN, rows, first, &tl); t += gridDim.x) {
+      FgTile tl = {};
+      for (long long t = blockIdx.x; fg_tile(t, a, BN, rows, first, &tl); t += gridDim.x) {
         const int nrow = min(FG_BM, tl.m_end - tl.m0), pieces = nrow > 96 ? 0 : (nrow + 31) / 32;
         const uint32_t bytes = ((pieces ? pieces * 32 : FG_BM) + BN) * FG_BK;
         const int wrow = tl.g * a.N + tl.n0;
@@ -630,8 +635,8 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
       const uint64_t desc0 = sw128_kmajor_desc(smem_u32(smem));
       int s = 0, as = 0, used = 0;
       uint32_t ph = 0, aph = 0;
-      FgTile tl;
-      for (long long t = blockIdx.x; fg_tile(t, a, FG_BM, BN, rows, first, &tl); t += gridDim.x) {
+      FgTile tl = {};
+      for (long long t = blockIdx.x; fg_tile(t, a, BN, rows, first, &tl); t += gridDim.x) {
         for (int kb = 0; kb < KB; ++kb) {
           pipe_wait(&full[s], ph, a.ctl, 0x414, gave_up);
           if (used == FW_SLOTS) {
@@ -669,8 +674,8 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
     const bool tma_out = (a.N & 7) == 0 && (reinterpret_cast<uintptr_t>(a.c) & 15) == 0;
     int as = 0;
     uint32_t aph = 0;
-    FgTile tl;
-    for (long long t = blockIdx.x; fg_tile(t, a, FG_BM, BN, rows, first, &tl); t += gridDim.x) {
+    FgTile tl = {};
+    for (long long t = blockIdx.x; fg_tile(t, a, BN, rows, first, &tl); t += gridDim.x) {
       const int row0 = tl.m0 + 32 * q, row = row0 + lane;
       const int col0 = tl.n0 + part * COLS;
       const bool idle = row0 >= tl.m_end || col0 >= a.N;
@@ -845,9 +850,7 @@ cudaError_t fg_launch_wide(const GemmArgs& a, long long tiles, cudaStream_t st) 
 cudaError_t launch_fp8_gemm(const GemmArgs& a, cudaStream_t st) {
   // row tiles: the groups hold M rows in all, each at most one partial tile
   const int groups = a.offsets ? (a.G < a.M ? a.G : a.M) : 1;
-  auto row_tiles = [&](int bm) -> long long {
-    return a.offsets ? a.M / bm + groups : (a.M + bm - 1) / bm;
-  };
+  const long long mt = a.offsets ? a.M / FG_BM + groups : (a.M + FG_BM - 1) / FG_BM;
   const long long avg = (a.M + groups - 1) / groups;
   const long long rows = avg >= FG_BM ? FG_BM : (avg + 31) / 32 * 32;
   const bool few = a.M <= 32;      // no tile has more than 32 rows
@@ -855,7 +858,7 @@ cudaError_t launch_fp8_gemm(const GemmArgs& a, cudaStream_t st) {
   long long best = 0, tiles = 0;
   int bn = 0;
   for (int b = 128; b >= 16; b >>= 1) {
-    const long long t = row_tiles(FG_BM) * ((a.N + b - 1) / b);
+    const long long t = mt * ((a.N + b - 1) / b);
     const long long cost = (t + sms - 1) / sms * (rows + b + 32);
     if (bn == 0 || cost < best) {
       best = cost;
@@ -864,7 +867,7 @@ cudaError_t launch_fp8_gemm(const GemmArgs& a, cudaStream_t st) {
     }
   }
   if (!few) {
-    const long long t = row_tiles(FG_BM) * ((a.N + 255) / 256);
+    const long long t = mt * ((a.N + 255) / 256);
     const long long cost = (t + sms - 1) / sms * (rows + 256 + 32);
     if (cost < best) return fg_launch_wide(a, t, st);
   }
