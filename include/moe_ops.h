@@ -19,7 +19,9 @@
  * Conventions are those of moe.h: pointers marked "dev" are caller-owned
  * memory of the current device; nothing allocates, frees or synchronises;
  * arguments are checked on the host before anything is enqueued on `stream`;
- * MOE_OK means "enqueued".  Calls may be captured into graphs.
+ * MOE_OK means "enqueued".  Calls may be captured into graphs, and several
+ * threads may call at once (on workspaces of their own).  Rows (T, M) are limited
+ * to 2^31 - 256, else MOE_ERR_UNSUPPORTED_SHAPE.
  *
  * e4m3: sign, 4 exponent bits (bias 7), 3 mantissa bits, largest value 448, no
  * infinity; codes 0x7F and 0xFF are NaN.

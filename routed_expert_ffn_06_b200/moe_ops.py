@@ -23,8 +23,8 @@ from .moe import MoEError, _check, _ptr
 
 # The current device and a device's current stream as plain integers: torch's
 # public calls build objects on the way (3 us for a stream, as long as a launch).
-_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_device = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 NORM_F_POST = 1
 NORM_F_ZERO_CENTRED = 2
@@ -126,12 +126,25 @@ def _blocks(n: int) -> int:
 
 
 class _Handle:
-    """A C struct, its address, and the tensors it points to."""
+    """A C struct, its address, the tensors it points to and their device (None
+    without any)."""
 
     def __init__(self, struct, *keep):
         self.struct = struct
         self.ref = ctypes.addressof(struct)
         self.keep = keep
+        self.dev = next((t.get_device() for t in keep if t is not None), None)
+
+    def here(self, dev):
+        if self.dev is not None and self.dev != dev:
+            raise ValueError(f"weights on cuda:{self.dev}, not on the current CUDA device")
+
+
+def _workspace(ws, dev):
+    """Address of a workspace: dense bytes on the current device."""
+    if ws is None:
+        return None
+    return _need(ws, "ws", (torch.uint8,), (ws.numel(),), dev)
 
 
 # ------------------------------------------------------------------- norms
@@ -159,6 +172,7 @@ def moe_norm_block(n: _Handle, x, y, gate, T: int, x_out=None, h=None, codes=Non
     y, gate ("full"), x_out, h: [T, d] with dense rows and any row pitch the
     library takes; y may be None."""
     s, ref, dev = n.struct, n.ref, _current()
+    n.here(dev)
     d, kind = s.d, s.gate_kind
     sdt, rows = _F32 if s.flags & NORM_F_STREAM_F32 else _BF16, (T, d)
     px = _need(x, "x", sdt, rows, dev, True)
@@ -216,6 +230,7 @@ def moe_fp8_quant(x, codes, scales, stream=None) -> None:
 
 
 def _products(w, a, a_scales, M, c, dev):
+    w.here(dev)
     s = w.struct
     k = s.k
     return (_need(a, "a", _E4M3, (M, k), dev),
@@ -229,8 +244,8 @@ def moe_fp8_gemm(w: _Handle, a, a_scales, M: int, c, ws=None, stream=None) -> No
     pa, psa, pc = _products(w, a, a_scales, M, c, dev)
     if M == 0:
         return
-    _check(load().moe_fp8_gemm(w.ref, pa, psa, M, pc, _ptr(ws), _stream(stream, dev)),
-           "moe_fp8_gemm")
+    _check(load().moe_fp8_gemm(w.ref, pa, psa, M, pc, _workspace(ws, dev),
+                               _stream(stream, dev)), "moe_fp8_gemm")
 
 
 def moe_fp8_gemm_grouped(w: _Handle, a, a_scales, M: int, offsets, c, ws=None, stream=None) -> None:
@@ -240,7 +255,8 @@ def moe_fp8_gemm_grouped(w: _Handle, a, a_scales, M: int, offsets, c, ws=None, s
     po = _need(offsets, "offsets", _I32, (w.struct.groups + 1,), dev)
     if M == 0:
         return
-    _check(load().moe_fp8_gemm_grouped(w.ref, pa, psa, M, po, pc, _ptr(ws), _stream(stream, dev)),
+    _check(load().moe_fp8_gemm_grouped(w.ref, pa, psa, M, po, pc, _workspace(ws, dev),
+                                       _stream(stream, dev)),
            "moe_fp8_gemm_grouped")
 
 
@@ -291,11 +307,12 @@ def alloc_fp8_workspace(layer: _Handle, max_tokens: int, device=None) -> torch.T
 def moe_fp8_layer_forward(layer: _Handle, x, T: int, y, ws, ids=None, w=None, stream=None) -> None:
     """The whole layer for up to FP8_LAYER_MAX_T tokens (include/moe_ops.h)."""
     s, dev = layer.struct, _current()
+    layer.here(dev)
     px = _need(x, "x", _BF16, (T, s.d_model), dev)
     py = _need(y, "y", _BF16, (T, s.d_model), dev)
     pi = None if ids is None else _need(ids, "ids", _I32, (T, s.top_k), dev)
     pw = None if w is None else _need(w, "w", _F32, (T, s.top_k), dev)
     if T == 0:
         return
-    _check(load().moe_fp8_layer_forward(layer.ref, px, T, py, pi, pw, _ptr(ws), ws.numel(),
-                                        _stream(stream, dev)), "moe_fp8_layer_forward")
+    _check(load().moe_fp8_layer_forward(layer.ref, px, T, py, pi, pw, _workspace(ws, dev),
+                                        ws.numel(), _stream(stream, dev)), "moe_fp8_layer_forward")

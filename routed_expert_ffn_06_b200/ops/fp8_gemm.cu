@@ -804,7 +804,7 @@ cudaError_t fg_launch(const GemmArgs& a, long long tiles, cudaStream_t st) {
       !fg_map(&mp.w, a.w, (uint64_t)a.K, (uint64_t)a.N * a.G, BN))
     return cudaErrorInvalidValue;
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(fp8_gemm_kernel<BN, AR>),
-                                   FgCfg<BN, AR>::smem(a.G));
+                                   kMaxSmem);
   if (e != cudaSuccess) return e;
   const long long grid = tiles < sm_count() ? tiles : sm_count();
   return launch_pdl(fp8_gemm_kernel<BN, AR>, dim3((unsigned)grid), dim3(FG_THREADS),
@@ -832,9 +832,9 @@ cudaError_t fg_launch_wide(const GemmArgs& a, long long tiles, cudaStream_t st) 
   if (e != cudaSuccess) return e;
   if (at.numRegs != FW_REGS) return cudaErrorInvalidConfiguration;
   // the offsets of very many groups take the place of one stage
-  const int stages = fw_smem(FW_MAX_STAGES, a.G) <= 227 * 1024 ? FW_MAX_STAGES : FW_MAX_STAGES - 1;
+  const int stages = fw_smem(FW_MAX_STAGES, a.G) <= kMaxSmem ? FW_MAX_STAGES : FW_MAX_STAGES - 1;
   const size_t sm = fw_smem(stages, a.G);
-  e = allow_smem(reinterpret_cast<const void*>(fp8_gemm_wide_kernel), sm);
+  e = allow_smem(reinterpret_cast<const void*>(fp8_gemm_wide_kernel), kMaxSmem);
   if (e != cudaSuccess) return e;
   const long long grid = tiles < sm_count() ? tiles : sm_count();
   return launch_pdl(fp8_gemm_wide_kernel, dim3((unsigned)grid), dim3(FW_THREADS), sm, st, a, stages,

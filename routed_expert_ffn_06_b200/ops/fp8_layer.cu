@@ -762,7 +762,7 @@ cudaError_t launch_fp8_layer(const Fp8LayerDev& L, const uint16_t* x, int T, uin
   cfg.numAttrs = 1;
   cfg.dynamicSmemBytes = (size_t)blocks128(L.d) * 4 * 32 * sizeof(uint4) + FL_WARPS * FL_RING;
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(fp8_layer_kernel),
-                                   cfg.dynamicSmemBytes);
+                                   FL_MAX_KB * 128 * sizeof(uint4) + FL_WARPS * FL_RING);
   if (e != cudaSuccess) return e;
   return cudaLaunchKernelEx(&cfg, fp8_layer_kernel, a);
 }

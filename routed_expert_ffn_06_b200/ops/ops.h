@@ -14,8 +14,12 @@ constexpr float kE4m3Max = 448.f;
 
 __host__ __device__ inline int blocks128(int n) { return (n + kBlock128 - 1) / kBlock128; }
 
-// Let a kernel use that much dynamic shared memory.
-cudaError_t allow_smem(const void* kernel, size_t bytes);
+// Let a kernel use up to that much dynamic shared memory: the same number in every
+// call, so that calls of several threads do not take it from one another.
+cudaError_t allow_smem(const void* kernel, size_t most);
+constexpr size_t kMaxSmem = 227 * 1024;  // of a block, static included
+// Rows of one call: below 2^31 with room for a rounding up to tiles.
+constexpr int kMaxRows = 0x7FFFFF00;
 
 struct NormArgs {
   int d, T;

@@ -36,6 +36,7 @@ moe_status gemm(const moe_fp8_mat* w, const uint8_t* a, const float* a_scales, i
   moe_status s = validate_mat(w);
   if (s != MOE_OK) return s;
   if (M < 0 || !a || !a_scales || !c) return MOE_ERR_INVALID_ARG;
+  if (M > kMaxRows) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (!offsets && w->groups != 1) return MOE_ERR_INVALID_ARG;
   if (!aligned(a, 16) || !aligned(a_scales, 4) || !aligned(c, 2) || !aligned(offsets, 4) ||
       !aligned(ws, 256))
@@ -101,8 +102,8 @@ Fp8LayerDev to_dev(const moe_fp8_layer* l) {
 
 }  // namespace
 
-cudaError_t allow_smem(const void* kernel, size_t bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+cudaError_t allow_smem(const void* kernel, size_t most) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
 }
 
 }  // namespace moe
@@ -123,7 +124,7 @@ moe_status moe_norm_block(const moe_norm* n, const void* x, const void* y_or_nul
   if (!(n->eps > 0.f) || !isfinite(n->eps) || !isfinite(n->stream_scale) ||
       !isfinite(n->branch_scale))
     return MOE_ERR_INVALID_ARG;
-  if (n->d < 8 || n->d > 8192 || n->d % 8) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (n->d < 8 || n->d > 8192 || n->d % 8 || T > kMaxRows) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (!codes_or_null != !scales_or_null) return MOE_ERR_INVALID_ARG;
   if (!x_out_or_null && !h_or_null && !codes_or_null) return MOE_ERR_INVALID_ARG;
   const bool gated = y_or_null && n->gate_kind != MOE_GATE_NONE;
@@ -172,7 +173,7 @@ moe_status moe_norm_block(const moe_norm* n, const void* x, const void* y_or_nul
 moe_status moe_fp8_quant(const void* x, int64_t ld, int32_t T, int32_t d, uint8_t* codes,
                          float* scales, void* stream) {
   if (!x || !codes || !scales || T < 0) return MOE_ERR_INVALID_ARG;
-  if (d < 8 || d > 65536 || d % 8) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (d < 8 || d > 65536 || d % 8 || T > kMaxRows) return MOE_ERR_UNSUPPORTED_SHAPE;
   long long p;
   if (!pitch(ld, d, &p)) return MOE_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(codes, 8) || !aligned(scales, 4)) return MOE_ERR_MISALIGNED;

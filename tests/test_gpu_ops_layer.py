@@ -178,6 +178,48 @@ def test_norm_layer_norm():
     assert ((h2.double() - h64).abs() <= BF16 * h64.abs() + dh * 1.01).all()
 
 
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_clean():
+    """The grid's first counter starts so low that the blocks' arrivals do not
+    reach the count they wait for: every block's wait ends after the limit, the
+    error word says so, and the counters are back where the next call needs them."""
+    L = Layer64(256, 32, 4, 64, 64, seed=3)
+    x = tokens(4, 256, 1)
+    y, ids, w, ws = L.run(x)
+    moe.moe_workspace_set_wait_limit(ws, 2000)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    ws[:256].view(torch.int32)[6] = -sms                  # the control block's first free word
+    L.run(x, ws)
+    torch.cuda.synchronize()
+    assert moe.moe_workspace_error(ws) == (7, 1)          # timeout
+    y2, ids2, w2, _ = L.run(x, ws)
+    assert torch.equal(y, y2) and torch.equal(ids, ids2) and torch.equal(w, w2)
+    assert moe.moe_workspace_error(ws) == (0, 0)
+
+
+def test_two_threads_call_at_once():
+    """Layers of different widths (different shared memory) from two threads."""
+    import threading
+    Ls = [Layer64(64, 8, 2, 32, 32, seed=1), Layer64(4096, 8, 2, 32, 32, seed=2)]
+    xs = [tokens(3, L.d, 5) for L in Ls]
+    refs = [L.run(x) for L, x in zip(Ls, xs)]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(L, x, ref):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(30):
+                y, _, _, ws = L.run(x, ref[3])
+                torch.cuda.current_stream().synchronize()
+                if not torch.equal(y, ref[0]):
+                    bad.append(L.d)
+    ts = [threading.Thread(target=work, args=a) for a in zip(Ls, xs, refs)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    assert not bad
+
+
 def test_refusals():
     L = Layer64(64, 8, 2, 32, 32, seed=1)
     ws = moe_ops.alloc_fp8_workspace(L.handle, 32)

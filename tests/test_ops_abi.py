@@ -59,7 +59,7 @@ def test_norm_arguments(lib):
     assert call_norm(lib, n) == OK
     assert call_norm(lib, n, x=None) == 1
     assert lib.moe_norm_block(None, X, Y, None, 0, XO, H, None, None, None) == 1
-    assert call_norm(lib, n, T=-1) == 1
+    assert call_norm(lib, n, T=-1) == 1 and call_norm(lib, n, T=2**31 - 1) == 2
     assert call_norm(lib, n, xo=None, h=None) == 1                # no output
     assert call_norm(lib, n, c=C) == 1 and call_norm(lib, n, s=S) == 1
     assert call_norm(lib, n, c=C, s=S) == OK
@@ -86,7 +86,7 @@ def test_quant_arguments(lib):
     assert f(X, 136, 0, 128, C, S, None) == OK
     assert f(X, 64, 0, 128, C, S, None) == 1 and f(X, 132, 0, 128, C, S, None) == 1
     assert f(None, 0, 1, 128, C, S, None) == 1 and f(X, 0, 1, 128, None, S, None) == 1
-    assert f(X, 0, -1, 128, C, S, None) == 1
+    assert f(X, 0, -1, 128, C, S, None) == 1 and f(X, 0, 2**31 - 1, 128, C, S, None) == 2
     assert f(X, 0, 1, 132, C, S, None) == 2 and f(X, 0, 1, 65544, C, S, None) == 2
     assert f(X + 2, 0, 1, 128, C, S, None) == 4 and f(X, 0, 1, 128, C + 4, S, None) == 4
 
@@ -109,7 +109,7 @@ def test_gemm_arguments(lib):
     assert f(mat(groups=2)) == 1                                  # groups need offsets
     assert lib.moe_fp8_gemm(None, X, G, 0, Y, None, None) == 1
     assert f(mat(), a=None) == 1 and f(mat(), sa=None) == 1 and f(mat(), c=None) == 1
-    assert f(mat(), M=-1) == 1
+    assert f(mat(), M=-1) == 1 and f(mat(), M=2**31 - 1) == 2
     assert f(mat(), a=X + 8) == 4 and f(mat(), c=Y + 1) == 4 and f(mat(), ws=WS + 16) == 4
     assert f(mat(), c=Y + 2) == OK
 
