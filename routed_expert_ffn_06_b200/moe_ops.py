@@ -100,12 +100,10 @@ def _stream(stream, dev):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _need(t, name, dtypes, shape, dev, rows_only=False):
+def _need(t, name, dtypes, shape, dev):
     """Check one tensor: on the current device `dev`, of one of dtypes, of the
-    shape given, dense (or, with rows_only, rows dense and any row pitch).
-    Returns its address."""
-    if t.dtype in dtypes and t.get_device() == dev and t.shape == shape and (
-            t.is_contiguous() or (rows_only and (t.shape[1] == 1 or t.stride(1) == 1))):
+    shape given, dense.  Returns its address."""
+    if t.dtype in dtypes and t.get_device() == dev and t.shape == shape and t.is_contiguous():
         return t.data_ptr()
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: {t.dtype}, expected {' or '.join(map(str, dtypes))}")
@@ -113,7 +111,21 @@ def _need(t, name, dtypes, shape, dev, rows_only=False):
         raise ValueError(f"{name}: on {t.device}, not on the current CUDA device")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    raise ValueError(f"{name}: {'rows are not dense' if rows_only else 'not contiguous'}")
+    raise ValueError(f"{name}: not contiguous")
+
+
+def _rows(t, name, dtypes, shape, dev, pitched):
+    """The same for rows that are dense themselves but may have any pitch, which
+    is noted in the dict `pitched` where it is not the row's length."""
+    if t.dtype in dtypes and t.get_device() == dev and t.shape == shape:
+        if t.is_contiguous():
+            return t.data_ptr()
+        if shape[1] == 1 or t.stride(1) == 1:
+            if shape[0] > 1:
+                pitched[name + "_ld"] = t.stride(0)
+            return t.data_ptr()
+        raise ValueError(f"{name}: rows are not dense")
+    return _need(t, name, dtypes, shape, dev)
 
 
 def _current():
@@ -175,31 +187,27 @@ def moe_norm_block(n: _Handle, x, y, gate, T: int, x_out=None, h=None, codes=Non
     n.here(dev)
     d, kind = s.d, s.gate_kind
     sdt, rows = _F32 if s.flags & NORM_F_STREAM_F32 else _BF16, (T, d)
-    px = _need(x, "x", sdt, rows, dev, True)
-    py = None if y is None else _need(y, "y", _BF16, rows, dev, True)
+    pitched = {}
+    px = _rows(x, "x", sdt, rows, dev, pitched)
+    py = None if y is None else _rows(y, "y", _BF16, rows, dev, pitched)
     pg = None
     if gate is not None and kind:
-        pg = _need(gate, "gate", _BF16, rows if kind == 3 else (T,) if kind == 1 else (d,), dev,
-                   kind == 3)
-    po = None if x_out is None else _need(x_out, "x_out", sdt, rows, dev, True)
-    ph = None if h is None else _need(h, "h", _BF16, rows, dev, True)
+        pg = _rows(gate, "gate", _BF16, rows, dev, pitched) if kind == 3 else \
+            _need(gate, "gate", _BF16, (T,) if kind == 1 else (d,), dev)
+    po = None if x_out is None else _rows(x_out, "x_out", sdt, rows, dev, pitched)
+    ph = None if h is None else _rows(h, "h", _BF16, rows, dev, pitched)
     pc = None if codes is None else _need(codes, "codes", _E4M3, rows, dev)
-    ps = None if scales is None else _need(scales, "scales", _F32, (T, _blocks(d)), dev)
+    ps = None if scales is None else _need(scales, "scales", _F32, (T, (d + 127) // 128), dev)
     if T == 0:   # an empty tensor has no address to pass
         return
-    if T > 1:
-        pitched = {}
-        for name, t in (("x_ld", x), ("y_ld", y), ("gate_ld", gate if kind == 3 else None),
-                        ("x_out_ld", x_out), ("h_ld", h)):
-            if t is not None and t.stride(0) != d:
-                pitched[name] = t.stride(0)
-        if pitched:   # the handle itself is never written: calls may share it
-            s = moe_norm.from_buffer_copy(s)
-            for name, v in pitched.items():
-                setattr(s, name, v)
-            ref = ctypes.addressof(s)
-    _check(load().moe_norm_block(ref, px, py, pg, T, po, ph, pc, ps, _stream(stream, dev)),
-           "moe_norm_block")
+    if pitched:  # the handle itself is never written: calls may share it
+        s = moe_norm.from_buffer_copy(s)
+        for name, v in pitched.items():
+            setattr(s, name, v)
+        ref = ctypes.addressof(s)
+    st = (_lib or load()).moe_norm_block(ref, px, py, pg, T, po, ph, pc, ps, _stream(stream, dev))
+    if st:
+        raise MoEError(st, "moe_norm_block")
 
 
 # ---------------------------------------------------------------- products
@@ -220,12 +228,13 @@ def moe_fp8_quant(x, codes, scales, stream=None) -> None:
     if x.dim() != 2:
         raise ValueError("x: [T, d]")
     (T, d), dev = x.shape, _current()
-    px = _need(x, "x", _BF16, x.shape, dev, True)
+    pitched = {}
+    px = _rows(x, "x", _BF16, x.shape, dev, pitched)
     pc = _need(codes, "codes", _E4M3, (T, d), dev)
     ps = _need(scales, "scales", _F32, (T, _blocks(d)), dev)
     if T == 0:
         return
-    _check(load().moe_fp8_quant(px, x.stride(0) if T > 1 else 0, T, d, pc, ps,
+    _check(load().moe_fp8_quant(px, pitched.get("x_ld", 0), T, d, pc, ps,
                                 _stream(stream, dev)), "moe_fp8_quant")
 
 

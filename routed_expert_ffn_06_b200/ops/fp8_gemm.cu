@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(FG_THREADS, 1) fp8_gemm_kernel(
     tmem_alloc(holder, C::kTmemCols);
     tmem_relinquish();
   }
-  if (warp == 0 && lane < 3)
+  if (warp == 0 && lane < 3 && (AR == FG_BM || lane > 0))
     asm volatile("prefetch.tensormap [%0];" ::"l"(
                      reinterpret_cast<uint64_t>(lane == 0 ? &mp.a : lane == 1 ? &mp.a32 : &mp.w))
                  : "memory");
@@ -799,7 +799,7 @@ bool fg_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uin
 template <int BN, int AR>
 cudaError_t fg_launch(const GemmArgs& a, long long tiles, cudaStream_t st) {
   FgMaps mp = {};
-  if (!fg_map(&mp.a, a.a, (uint64_t)a.K, (uint64_t)a.M, FG_BM) ||
+  if ((AR == FG_BM && !fg_map(&mp.a, a.a, (uint64_t)a.K, (uint64_t)a.M, FG_BM)) ||
       !fg_map(&mp.a32, a.a, (uint64_t)a.K, (uint64_t)a.M, 32) ||
       !fg_map(&mp.w, a.w, (uint64_t)a.K, (uint64_t)a.N * a.G, BN))
     return cudaErrorInvalidValue;
