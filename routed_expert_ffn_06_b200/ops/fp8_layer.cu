@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(FL_THREADS, 1) fp8_layer_kernel(FlArgs a) {
   __shared__ uint2 s_cand[FL_T][32];
   __shared__ uint32_t s_bits[32];
   __shared__ int s_pre[32];
-  __shared__ int s_list[FL_MAX_U];             // unique experts, ascending
+  __shared__ int s_list[FL_MAX_U];             // the window's experts, each once
   // routing weight of (expert, token) in phase 3; scale of its hidden values in
   // phase 4, the shared expert's at U
   __shared__ float s_mix[FL_MAX_U + 1][FL_T];
@@ -535,7 +535,15 @@ __global__ void __launch_bounds__(FL_THREADS, 1) fp8_layer_kernel(FlArgs a) {
                 s_ids[t0 + warp], s_w[t0 + warp], s_cand[warp]);
       __syncthreads();
     }
-    if (warp == 0) {
+    if (T == 1) {
+      // a single token's experts are its list, in its order
+      if (tid < L.k) {
+        s_list[tid] = s_ids[0][tid];
+        s_mix[tid][0] = s_w[0][tid];
+        s_sel[tid] = 1u;
+        if (tid == 0) s_u = L.k;
+      }
+    } else if (warp == 0) {
       // the unique experts in ascending order: a bitmap and its prefix counts
       for (int i = lane; i < T * L.k; i += 32) {
         const int e = s_ids[i / L.k][i % L.k];
@@ -559,7 +567,8 @@ __global__ void __launch_bounds__(FL_THREADS, 1) fp8_layer_kernel(FlArgs a) {
         s_mix[u][t] = s_w[t][j];
         atomicOr(&s_sel[u], 1u << t);
       }
-    } else if (warp == 1 && blockIdx.x == 0) {
+    }
+    if (warp == 1 && blockIdx.x == 0) {
       for (int i = lane; i < T * L.k; i += 32) {
         if (a.ids) a.ids[i] = s_ids[i / L.k][i % L.k];
         if (a.w) a.w[i] = s_w[i / L.k][i % L.k];
@@ -638,6 +647,8 @@ __global__ void __launch_bounds__(FL_THREADS, 1) fp8_layer_kernel(FlArgs a) {
     grid_wait(&sy->hidden, nblk, a.ctl, 0x501);
   }
   __syncthreads();
+  float4 h[2][8];                              // hidden values, one item ahead
+  if (blockIdx.x < tiles) load_h(h[0], start());
   for (int i = tid; i < down_end * FL_T; i += FL_THREADS) {
     const int u = i >> 3, t = i & 7;
     const int top = (int)(__ldcg(u < U ? &a.top[i] : &sy->shared_top[t]) >> 23);
@@ -650,8 +661,7 @@ __global__ void __launch_bounds__(FL_THREADS, 1) fp8_layer_kernel(FlArgs a) {
     const int row0 = 16 * r;
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
     Item m = start(), ahead = m, hm = m;
-    float4 h[2][8];                            // hidden values, one item ahead
-    load_h(h[0], hm);
+    if (r != blockIdx.x) load_h(h[0], hm);
     for (int i = 0; i < FL_DEPTH4; ++i) {
       if (r != blockIdx.x) ask_w(i, ahead, row0);
       step(ahead);
