@@ -11,15 +11,15 @@
 // owns one row and columns of a single 128-row weight block.
 //
 // A tile is 128 rows x BN columns.  Warp 0 loads the A and W tiles of each
-// block by TMA (128-byte swizzle: a row of a block is exactly one 128-byte
-// atom), one lane of warp 1 issues the MMAs, the other warps promote: two (BN = 256:
-// four) per TMEM lane quarter, each with its part of the columns.  TMEM holds 512 / BN
-// accumulators (two at BN = 256), so the MMAs of the next block run while one
+// k-block by TMA (128-byte swizzle: a row of a k-block is exactly one 128-byte
+// atom), one lane of warp 1 issues the MMAs, eight other warps promote, two per
+// TMEM lane quarter, each with half of the columns.  TMEM holds several
+// accumulators (two at BN = 256), so the MMAs of the next k-blocks run while one
 // is promoted.  Blocks are persistent over tiles.
 //
-// BN = 256 keeps the tensor cores busiest per byte of shared memory; narrow
-// tiles (down to 16) spread few rows over all SMs, which then stream the
-// weights at HBM rate.  The rule is in launch_fp8_gemm.
+// Two kernels: fp8_gemm_kernel for BN = 16 .. 128, where few rows are spread over
+// all SMs, which then stream the weights; fp8_gemm_wide_kernel for BN = 256, which
+// moves the fewest operand bytes per product.  The rule is in launch_fp8_gemm.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -518,9 +518,11 @@ __global__ void __launch_bounds__(FG_THREADS, 1) fp8_gemm_kernel(
 // ------------------------------------------------------------ wide tiles
 // 128 x 256 tiles for many rows.  The L2 delivers about 68 bytes per cycle and SM
 // (measured), so a k-block's 48 KB take 720 cycles, against 540 of the MMAs; 128 x
-// 128 tiles would need 480 cycles for 270.  (Pairs of SMs on 256 x 256 tiles load
-// 32 KB per SM and k-block, but the hand-overs between two SMs cost more than that
-// saves: 65 us for 8192 x 4096 x 2048, with the same four accumulators.)
+// 128 tiles would need 480 cycles for 270.  Measured: 8192 x 4096 x 2048 in 67 us
+// (2.05 PFLOP/s in a short run), 20,480 rows in 512 groups of 1024 x 2048 in 198 us
+// (5.8 TB/s of weights).  Pairs of SMs on 256 x 256 tiles load 32 KB per SM and
+// k-block, but the hand-overs between two SMs cost what that saves: 65 us for the
+// first, and 420 against 305 us for 81,920 rows in 512 groups.
 //
 // One tcgen05.mma takes all 256 columns: at 128 columns a block's MMAs read A
 // twice and shared memory at 122 bytes per cycle, which nearly halves their rate.
