@@ -655,7 +655,10 @@ __global__ void __launch_bounds__(FL_THREADS, 1) fp8_layer_kernel(FlArgs a) {
     const int u = i >> 3, t = i & 7;
     const int top = (int)(__ldcg(u < U ? &a.top[i] : &sy->shared_top[t]) >> 23);
     const int e = top == 255 ? 0 : min(141 - top, 120);      // as the tokens', to 2^14..2^15
-    s_mix[u][t] = __uint_as_float((uint32_t)(e + 127) << 23);
+    // 0 marks a token that did not select the expert: whatever the expert's weights
+    // are, NaN included, the token's sums leave its products out
+    const bool on = u < U ? (s_sel[u] >> t) & 1u : t < T;
+    s_mix[u][t] = on ? __uint_as_float((uint32_t)(e + 127) << 23) : 0.f;
   }
   __syncthreads();
 
@@ -701,7 +704,9 @@ __global__ void __launch_bounds__(FL_THREADS, 1) fp8_layer_kernel(FlArgs a) {
           }
         }
 #pragma unroll
-        for (int c = 0; c < 4; ++c) sum[c] = fmaf(acc[0][c] + acc[1][c], c & 1 ? i1 : i0, sum[c]);
+        for (int c = 0; c < 4; ++c)
+          if ((c & 1 ? mx.y : mx.x) != 0.f)
+            sum[c] = fmaf(acc[0][c] + acc[1][c], c & 1 ? i1 : i0, sum[c]);
         ask_w(slot, ahead, row0);              // the slot's values are in registers
         step(ahead);
         step(m);

@@ -13,10 +13,10 @@
 // Rows of up to 512 channels take one warp each (no block barrier); wider rows
 // take a block each, of as many threads as chunks (measured: 777 x 1000 channels
 // 3.9 us against 6.6 us with a warp per row, 8192 x 1024 18.1 against 22.6; at
-// 30,000 x 512 the warps win, 22.8 against 32.4).  Blocks
-// that walk the rows, with the weights in registers and the next row on its way,
-// gained 2% at 8192 x 2048 and lost 20% at 8192 x 1024.  128 channels are 16 chunks = 16 consecutive lanes,
-// so the largest |h| of a scale block is a half-warp maximum.
+// 30,000 x 512 the warps win, 22.8 against 32.4).  Blocks that walk the rows,
+// with the weights in registers and the next row on its way, gained 2% at
+// 8192 x 2048 and lost 20% at 8192 x 1024.  128 channels are 16 chunks = 16
+// consecutive lanes, so the largest |h| of a scale block is a half-warp maximum.
 #include "ops.h"
 
 namespace moe {

@@ -44,9 +44,9 @@ def test_dense(M, N, K):
 
 
 def test_each_tile_width_is_reached():
-    """One row of tiles per width: 148 SMs of a B200 take 16 columns up to
-    147 x 32 columns and 256 from 148 x 256 on; the widths between follow from
-    the rule in the launcher."""
+    """One row of tiles, from a few hundred columns to more than the widest tile
+    times the SMs of a B200: the launcher's cost estimate goes from the
+    narrowest tile to the widest."""
     for N in (512, 148 * 32, 148 * 64, 148 * 128, 148 * 256):
         dense(100, N + 3, 272, seed=N)
 

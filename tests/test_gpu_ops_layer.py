@@ -107,6 +107,27 @@ def test_a_nan_token_keeps_to_itself():
     L.check(x[keep], y[keep], ids[keep], w[keep])
 
 
+@pytest.mark.parametrize("what", ["codes", "scales"])
+@pytest.mark.parametrize("part", ["gu", "dn"])
+def test_nan_weights_reach_only_the_tokens_of_their_expert(part, what):
+    """NaN or infinity in one expert's weights: the rows of the tokens that did
+    not select it keep every bit."""
+    L = Layer64(512, 32, 4, 128, 128, seed=12)
+    x = tokens(8, 512, 13)
+    y, ids, w, ws = L.run(x)
+    count = torch.bincount(ids.flatten().long(), minlength=32)
+    e = int(((count > 0) & (count < 8)).nonzero()[0])
+    if what == "codes":
+        getattr(L, part).view(torch.uint8)[e] = 0x7F
+    else:
+        getattr(L, part + "s")[e] = float("inf")
+    y2, i2, w2, _ = L.run(x, ws)
+    assert moe.moe_workspace_error(ws) == (0, 0)
+    hit = (ids == e).any(1)
+    assert torch.equal(ids, i2) and torch.equal(w, w2) and torch.equal(y[~hit], y2[~hit])
+    assert not torch.isfinite(y2[hit].float()).any()
+
+
 def test_large_and_small_values():
     L = Layer64(512, 32, 4, 128, 128, seed=8, router_std=1e-4)
     for scale in (300.0, 1e-3):
