@@ -332,10 +332,10 @@ __global__ void __launch_bounds__(FG_THREADS, 1) fp8_gemm_kernel(
                      reinterpret_cast<uint64_t>(lane == 0 ? &mp.a : lane == 1 ? &mp.a32 : &mp.w))
                  : "memory");
   pdl_wait();
-  pdl_launch_dependents();
   fg_groups(a, rows, first);
   tc_fence_before();
   __syncthreads();
+  pdl_launch_dependents();   // the TMEM is allocated: no block of the next kernel can take it first
   tc_fence_after();
   const uint32_t tmem = *holder;
   const bool elected = elect_one();
@@ -584,10 +584,10 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
                      reinterpret_cast<uint64_t>(lane == 0 ? &mp.a : lane == 1 ? &mp.a32 : &mp.w))
                  : "memory");
   pdl_wait();
-  pdl_launch_dependents();
   fg_groups(a, rows, first);
   tc_fence_before();
   __syncthreads();
+  pdl_launch_dependents();   // the TMEM is allocated: no block of the next kernel can take it first
   tc_fence_after();
   const uint32_t tmem = *holder;
   const bool elected = elect_one();
