@@ -7,13 +7,15 @@
 //                                           scale per 128 columns
 //
 // One pass over memory: a row stays in registers between the loads and the
-// stores, so every byte is read once and written once; the kernel is bound by
-// HBM for many rows and by its launch and two dependent reductions for one.
+// stores, so every byte is read once and written once.  Many rows are bound by
+// HBM without a gate and a quantiser (8192 x 2048: 6.0 TB/s) and by the
+// instructions issued with them (5.2 TB/s); one row by its launch and two
+// dependent reductions.
 // A thread owns chunks of 8 consecutive channels (16-byte accesses in bf16).
 // Rows of up to 512 channels take one warp each (no block barrier); wider rows
 // take a block each, of as many threads as chunks (measured: 777 x 1000 channels
-// 3.9 us against 6.6 us with a warp per row, 8192 x 1024 18.1 against 22.6; at
-// 30,000 x 512 the warps win, 22.8 against 32.4).  Blocks that walk the rows,
+// 3.9 us against 6.6 us with a warp per row, 8192 x 1024 17.5 against 22.6; at
+// 30,000 x 512 the warps win, 22.0 against 32.4).  Blocks that walk the rows,
 // with the weights in registers and the next row on its way, gained 2% at
 // 8192 x 2048 and lost 20% at 8192 x 1024.  128 channels are 16 chunks = 16
 // consecutive lanes, so the largest |h| of a scale block is a half-warp maximum.
@@ -23,28 +25,56 @@ namespace moe {
 
 namespace {
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&o)[8]) {
+// Channels are held in pairs: fp32 arithmetic on a pair is one instruction
+// (fma.rn.f32x2), each half rounded as alone.
+__device__ __forceinline__ unsigned long long bits64(float2 v) {
+  return *reinterpret_cast<const unsigned long long*>(&v);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits64(a)), "l"(bits64(b)), "l"(bits64(c)));
+  return *reinterpret_cast<float2*>(&d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits64(a)), "l"(bits64(b)));
+  return *reinterpret_cast<float2*>(&d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  unsigned long long d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits64(a)), "l"(bits64(b)));
+  return *reinterpret_cast<float2*>(&d);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+__device__ __forceinline__ void unpack8(const uint4& v, float2 (&o)[4]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    o[2 * j] = __uint_as_float(w[j] << 16);
-    o[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-  }
+  for (int j = 0; j < 4; ++j)
+    o[j] = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+__device__ __forceinline__ uint4 pack8(const float2 (&v)[4]) {
   uint32_t w[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v[j].x, v[j].y);
     w[j] = *reinterpret_cast<const uint32_t*>(&b);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__device__ __forceinline__ void load8f(const float* p, float (&o)[8]) {
+__device__ __forceinline__ void load8f(const float* p, float2 (&o)[4]) {
   const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w, o[4] = b.x, o[5] = b.y, o[6] = b.z, o[7] = b.w;
+  o[0] = make_float2(a.x, a.y), o[1] = make_float2(a.z, a.w);
+  o[2] = make_float2(b.x, b.y), o[3] = make_float2(b.z, b.w);
+}
+
+// max(|a|, |b|, |c|), NaN if one of them is.
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 // Four floats to four e4m3 codes, nearest with ties to even, clamped to +-448.
@@ -55,30 +85,30 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 
-// Quantise one chunk of 8 channels of a block of 16 lanes.  The maximum is
-// taken over the bit patterns of |v|, so that a NaN or infinity survives it.
-// `live`: the chunk lies inside the row (all lanes of the warp call this).
-__device__ __forceinline__ void quant8(const float (&v)[8], bool live, uint8_t* codes,
+// Quantise one chunk of 8 channels of a block of 16 lanes.  A NaN or infinity
+// survives the maximum.  `live`: the chunk lies inside the row (all lanes of the
+// warp call this).
+__device__ __forceinline__ void quant8(const float2 (&v)[4], bool live, uint8_t* codes,
                                        float* scale) {
-  uint32_t m = 0;
+  float top = 0.f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-  if (!live) m = 0;
+  for (int j = 0; j < 4; ++j) top = max3_abs(top, v[j].x, v[j].y);
+  if (!live) top = 0.f;
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float top = __uint_as_float(m), s = top * (1.f / kE4m3Max);
+  for (int o = 8; o > 0; o >>= 1) top = max3_abs(top, __shfl_xor_sync(0xffffffffu, top, o), 0.f);
+  const float s = top * (1.f / kE4m3Max);
   if (!live) return;
   // one division for the block; v / s would overflow it below about 1e-36
-  const float inv = kE4m3Max / fmaxf(top, 1e-30f);
-  float q[8];
+  const float2 inv = both(kE4m3Max / fmaxf(top, 1e-30f));
+  float2 q[4];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) q[j] = v[j] * inv;
+  for (int j = 0; j < 4; ++j) q[j] = mul2(v[j], inv);
   if (top < 1e-30f) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) q[j] = s != 0.f ? v[j] / s : v[j];
+    for (int j = 0; j < 4; ++j) q[j] = s != 0.f ? make_float2(v[j].x / s, v[j].y / s) : v[j];
   }
   *reinterpret_cast<uint2*>(codes) =
-      make_uint2(e4m3x4(q[0], q[1], q[2], q[3]), e4m3x4(q[4], q[5], q[6], q[7]));
+      make_uint2(e4m3x4(q[0].x, q[0].y, q[1].x, q[1].y), e4m3x4(q[2].x, q[2].y, q[3].x, q[3].y));
   if ((threadIdx.x & 15) == 0) *scale = s;
 }
 
@@ -100,8 +130,12 @@ __device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f +
 
 constexpr int kWarpRows = 4;   // rows (warps) of a block when a row takes one warp
 
+// 32 registers keep two blocks of 1024 threads, or eight of 256, on an SM: without
+// the bound the pairs take 37, and 2048 x 8192 channels 51 us in place of 40.  With
+// single floats 8192 x 2048 takes 37.1 us in place of 35.5, 30,000 x 512 22.7 in
+// place of 22.0, 2048 x 8192 38.6.
 template <bool F32, bool WARP_ROW, int CH>
-__global__ void __launch_bounds__(WARP_ROW ? 32 * kWarpRows : 1024) norm_block_kernel(NormArgs a) {
+__global__ void __launch_bounds__(WARP_ROW ? 32 * kWarpRows : 1024, WARP_ROW ? 1 : 2) norm_block_kernel(NormArgs a) {
   __shared__ float red[2][32];
   const int lane = WARP_ROW ? (threadIdx.x & 31) : threadIdx.x;
   const int nt = WARP_ROW ? 32 : blockDim.x;
@@ -110,7 +144,7 @@ __global__ void __launch_bounds__(WARP_ROW ? 32 * kWarpRows : 1024) norm_block_k
   pdl_launch_dependents();
   if (WARP_ROW && row >= a.T) return;
   const int nc = a.d >> 3;
-  float r[CH][8];          // the stream, then r
+  float2 r[CH][4];         // the stream, then r
   uint4 yv[CH], gv[CH];
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
@@ -121,7 +155,7 @@ __global__ void __launch_bounds__(WARP_ROW ? 32 * kWarpRows : 1024) norm_block_k
         load8f(static_cast<const float*>(a.x) + row * a.x_ld + 8 * c, r[i]);
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) r[i][j] = 0.f;
+        for (int j = 0; j < 4; ++j) r[i][j] = both(0.f);
       }
     } else {
       const uint4 xv = live ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) +
@@ -142,51 +176,52 @@ __global__ void __launch_bounds__(WARP_ROW ? 32 * kWarpRows : 1024) norm_block_k
   }
   float inv_y = 1.f;
   if (a.post) {
-    float ss = 0.f;
+    float2 ss = both(0.f);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      float v[8];
+      float2 v[4];
       unpack8(yv[i], v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
+      for (int j = 0; j < 4; ++j) ss = fma2(v[j], v[j], ss);
     }
-    inv_y = rsqrtf(row_sum<WARP_ROW>(ss, red[0]) * a.inv_d + a.eps);
+    inv_y = rsqrtf(row_sum<WARP_ROW>(ss.x + ss.y, red[0]) * a.inv_d + a.eps);
   }
-  float ss = 0.f;
+  float2 ss = both(0.f);
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = lane + i * nt;
-    float u[8], g[8];
+    float2 u[4], g[4];
     unpack8(yv[i], u);
     if (a.post) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) u[j] *= inv_y;
+      for (int j = 0; j < 4; ++j) u[j] = mul2(u[j], both(inv_y));
       if (a.post_w && c < nc) {
-        float w[8];
+        float2 w[4];
         load8f(a.post_w + 8 * c, w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) u[j] *= w[j] + a.w_off;
+        for (int j = 0; j < 4; ++j) u[j] = mul2(u[j], add2(w[j], both(a.w_off)));
       }
     }
     if (a.gate_kind >= MOE_GATE_CHANNEL) {
       unpack8(gv[i], g);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) u[j] *= a.sigmoid ? sigmoid(g[j]) : g[j];
+      for (int j = 0; j < 4; ++j)
+        u[j] = mul2(u[j], a.sigmoid ? make_float2(sigmoid(g[j].x), sigmoid(g[j].y)) : g[j]);
     } else if (a.gate_kind == MOE_GATE_TOKEN) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) u[j] *= gt;
+      for (int j = 0; j < 4; ++j) u[j] = mul2(u[j], both(gt));
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float x = a.a * r[i][j];
-      r[i][j] = a.y ? fmaf(a.b, u[j], x) : x;
-      ss = fmaf(r[i][j], r[i][j], ss);
+    for (int j = 0; j < 4; ++j) {
+      const float2 x = mul2(both(a.a), r[i][j]);
+      r[i][j] = a.y ? fma2(both(a.b), u[j], x) : x;
+      ss = fma2(r[i][j], r[i][j], ss);
     }
     if (a.x_out && c < nc) {
       if (F32) {
         float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.x_out) + row * a.x_out_ld + 8 * c);
-        o[0] = make_float4(r[i][0], r[i][1], r[i][2], r[i][3]);
-        o[1] = make_float4(r[i][4], r[i][5], r[i][6], r[i][7]);
+        o[0] = make_float4(r[i][0].x, r[i][0].y, r[i][1].x, r[i][1].y);
+        o[1] = make_float4(r[i][2].x, r[i][2].y, r[i][3].x, r[i][3].y);
       } else {
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.x_out) + row * a.x_out_ld + 8 * c) =
             pack8(r[i]);
@@ -194,18 +229,18 @@ __global__ void __launch_bounds__(WARP_ROW ? 32 * kWarpRows : 1024) norm_block_k
     }
   }
   if (!a.h && !a.codes) return;
-  const float inv = rsqrtf(row_sum<WARP_ROW>(ss, red[1]) * a.inv_d + a.eps);
+  const float inv = rsqrtf(row_sum<WARP_ROW>(ss.x + ss.y, red[1]) * a.inv_d + a.eps);
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = lane + i * nt;
     const bool live = c < nc;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) r[i][j] *= inv;
+    for (int j = 0; j < 4; ++j) r[i][j] = mul2(r[i][j], both(inv));
     if (a.pre_w && live) {
-      float w[8];
+      float2 w[4];
       load8f(a.pre_w + 8 * c, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) r[i][j] *= w[j] + a.w_off;
+      for (int j = 0; j < 4; ++j) r[i][j] = mul2(r[i][j], add2(w[j], both(a.w_off)));
     }
     if (a.h && live) *reinterpret_cast<uint4*>(a.h + row * a.h_ld + 8 * c) = pack8(r[i]);
     if (a.codes)
@@ -231,7 +266,7 @@ __global__ void __launch_bounds__(256) fp8_quant_kernel(const uint16_t* __restri
     const long long row = b / kb;
     const int cb = (int)(b - row * kb), c = cb * kBlock128 + 8 * l;
     const bool live = b < n && c < d;
-    float v[8];
+    float2 v[4];
     unpack8(live ? *reinterpret_cast<const uint4*>(x + row * ld + c) : make_uint4(0, 0, 0, 0), v);
     quant8(v, live, codes + row * d + c, scales + b);
   }
