@@ -596,12 +596,18 @@ __global__ void __launch_bounds__(FL_THREADS, 1) fp8_layer_kernel(FlArgs a) {
     m.kb = warp - m.u * KBf;
     return m;
   };
+  const int du = FL_WARPS / KBf, dk = FL_WARPS - du * KBf;
   auto step = [&](Item& m) {
     m.it += FL_WARPS;
-    m.kb += FL_WARPS;
-    while (m.u < U && m.kb >= KBf) {
+    m.u += du;
+    m.kb += dk;
+    if (m.kb >= KBf) {
       m.kb -= KBf;
       ++m.u;
+    }
+    if (m.it >= U * KBf) {
+      m.u = U;
+      m.kb = m.it - U * KBf;
     }
   };
   auto ask_w = [&](int slot, const Item& m, int row0) {
@@ -709,7 +715,7 @@ __global__ void __launch_bounds__(FL_THREADS, 1) fp8_layer_kernel(FlArgs a) {
             sum[c] = fmaf(acc[0][c] + acc[1][c], c & 1 ? i1 : i0, sum[c]);
         ask_w(slot, ahead, row0);              // the slot's values are in registers
         step(ahead);
-        step(m);
+        m = hm;
         if (++slot == FL_DEPTH4) slot = 0;
       }
     }
