@@ -268,7 +268,6 @@ __global__ void __launch_bounds__(FL_THREADS, 1) fp8_layer_kernel(FlArgs a) {
   __shared__ float s_w[FL_T][16];
   __shared__ uint2 s_cand[FL_T][32];
   __shared__ uint32_t s_bits[32];
-  __shared__ int s_pre[32];
   __shared__ int s_list[FL_MAX_U];             // the window's experts, each once
   // routing weight of (expert, token) in phase 3; scale of its hidden values in
   // phase 4, the shared expert's at U
@@ -532,9 +531,13 @@ __global__ void __launch_bounds__(FL_THREADS, 1) fp8_layer_kernel(FlArgs a) {
       for (int i = tid; i < n * L.E; i += FL_THREADS)
         keys[i] = order_key(__ldcg(a.logits + (size_t)t0 * L.E + i));
       __syncthreads();
-      if (warp < n)
-        fl_topk(keys + warp * L.E, a.logits + (size_t)(t0 + warp) * L.E, L.E, L.k,
-                s_ids[t0 + warp], s_w[t0 + warp], s_cand[warp]);
+      if (warp < n) {
+        const int t = t0 + warp;
+        fl_topk(keys + warp * L.E, a.logits + (size_t)t * L.E, L.E, L.k, s_ids[t], s_w[t],
+                s_cand[warp]);
+        __syncwarp();
+        if (lane < L.k) atomicOr(&s_bits[s_ids[t][lane] >> 5], 1u << (s_ids[t][lane] & 31));
+      }
       __syncthreads();
     }
     if (T == 1) {
@@ -545,29 +548,26 @@ __global__ void __launch_bounds__(FL_THREADS, 1) fp8_layer_kernel(FlArgs a) {
         s_sel[tid] = 1u;
         if (tid == 0) s_u = L.k;
       }
-    } else if (warp == 0) {
-      // the unique experts in ascending order: a bitmap and its prefix counts
-      for (int i = lane; i < T * L.k; i += 32) {
-        const int e = s_ids[i / L.k][i % L.k];
-        atomicOr(&s_bits[e >> 5], 1u << (e & 31));
-      }
-      __syncwarp();
-      const int n = __popc(s_bits[lane]);
+    } else if (warp < T) {
+      // the unique experts in ascending order: a bitmap and its prefix counts, by
+      // the warp of each token
+      const uint32_t bits = s_bits[lane];
+      const int n = __popc(bits);
       int v = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int up = __shfl_up_sync(0xffffffffu, v, o);
         if (lane >= o) v += up;
       }
-      s_pre[lane] = v - n;
-      if (lane == 31) s_u = v;
-      __syncwarp();
-      for (int i = lane; i < T * L.k; i += 32) {
-        const int t = i / L.k, j = i - t * L.k, e = s_ids[t][j];
-        const int u = s_pre[e >> 5] + __popc(s_bits[e >> 5] & ((1u << (e & 31)) - 1u));
-        s_list[u] = e;                      // equal values from every token that chose e
-        s_mix[u][t] = s_w[t][j];
-        atomicOr(&s_sel[u], 1u << t);
+      if (warp == 0 && lane == 31) s_u = v;
+      const int e = lane < L.k ? s_ids[warp][lane] : 0;
+      const int before = __shfl_sync(0xffffffffu, v - n, e >> 5);
+      const uint32_t same = __shfl_sync(0xffffffffu, bits, e >> 5);
+      if (lane < L.k) {
+        const int u = before + __popc(same & ((1u << (e & 31)) - 1u));
+        s_list[u] = e;                        // equal values from every token that chose e
+        s_mix[u][warp] = s_w[warp][lane];
+        atomicOr(&s_sel[u], 1u << warp);
       }
     }
     if (warp == 1 && blockIdx.x == 0) {
