@@ -122,6 +122,9 @@ def _rows(t, name, dtypes, shape, dev, pitched):
             return t.data_ptr()
         if shape[1] == 1 or t.stride(1) == 1:
             if shape[0] > 1:
+                # a pitch of 0 (an expanded row) would mean dense rows to the library
+                if t.stride(0) < shape[1]:
+                    raise ValueError(f"{name}: rows overlap")
                 pitched[name + "_ld"] = t.stride(0)
             return t.data_ptr()
         raise ValueError(f"{name}: rows are not dense")

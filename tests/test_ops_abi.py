@@ -178,6 +178,16 @@ def test_binding_refuses_host_tensors_and_wrong_types(lib):
         moe_ops.moe_fp8_quant(w.bfloat16(), w, w)
 
 
+def test_binding_takes_pitched_rows_and_refuses_overlapping_ones():
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    bf16, host, seen = (torch.bfloat16,), -1, {}
+    assert moe_ops._rows(x[:, :32], "x", bf16, (4, 32), host, seen) == x.data_ptr()
+    assert seen == {"x_ld": 64}
+    for t in (x[:1].expand(4, 64), x.view(-1).as_strided((4, 64), (32, 1)), x.t()):
+        with pytest.raises(ValueError):
+            moe_ops._rows(t, "x", bf16, tuple(t.shape), host, {})
+
+
 def test_header_compiles_as_c99_and_ctypes_mirrors_the_structs(tmp_path):
     gcc = shutil.which("gcc")
     if gcc is None:
