@@ -103,8 +103,11 @@ def _stream(stream, dev):
 def _need(t, name, dtypes, shape, dev):
     """Check one tensor: on the current device `dev`, of one of dtypes, of the
     shape given, dense.  Returns its address."""
-    if t.dtype in dtypes and t.get_device() == dev and t.shape == shape and t.is_contiguous():
-        return t.data_ptr()
+    try:
+        if t.dtype in dtypes and t.get_device() == dev and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        raise ValueError(f"{name}: {type(t).__name__}, expected a tensor") from None
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: {t.dtype}, expected {' or '.join(map(str, dtypes))}")
     if t.get_device() != dev:
@@ -117,17 +120,20 @@ def _need(t, name, dtypes, shape, dev):
 def _rows(t, name, dtypes, shape, dev, pitched):
     """The same for rows that are dense themselves but may have any pitch, which
     is noted in the dict `pitched` where it is not the row's length."""
-    if t.dtype in dtypes and t.get_device() == dev and t.shape == shape:
-        if t.is_contiguous():
-            return t.data_ptr()
-        if shape[1] == 1 or t.stride(1) == 1:
-            if shape[0] > 1:
-                # a pitch of 0 (an expanded row) would mean dense rows to the library
-                if t.stride(0) < shape[1]:
-                    raise ValueError(f"{name}: rows overlap")
-                pitched[name + "_ld"] = t.stride(0)
-            return t.data_ptr()
-        raise ValueError(f"{name}: rows are not dense")
+    try:
+        if t.dtype in dtypes and t.get_device() == dev and t.shape == shape:
+            if t.is_contiguous():
+                return t.data_ptr()
+            if shape[1] == 1 or t.stride(1) == 1:
+                if shape[0] > 1:
+                    # a pitch of 0 (an expanded row) would mean dense rows to the library
+                    if t.stride(0) < shape[1]:
+                        raise ValueError(f"{name}: rows overlap")
+                    pitched[name + "_ld"] = t.stride(0)
+                return t.data_ptr()
+            raise ValueError(f"{name}: rows are not dense")
+    except AttributeError:
+        pass   # no tensor: said below
     return _need(t, name, dtypes, shape, dev)
 
 
@@ -159,7 +165,7 @@ def _workspace(ws, dev):
     """Address of a workspace: dense bytes on the current device."""
     if ws is None:
         return None
-    return _need(ws, "ws", (torch.uint8,), (ws.numel(),), dev)
+    return _need(ws, "ws", (torch.uint8,), getattr(ws, "shape", None), dev)
 
 
 # ------------------------------------------------------------------- norms
@@ -324,6 +330,8 @@ def moe_fp8_layer_forward(layer: _Handle, x, T: int, y, ws, ids=None, w=None, st
     py = _need(y, "y", _BF16, (T, s.d_model), dev)
     pi = None if ids is None else _need(ids, "ids", _I32, (T, s.top_k), dev)
     pw = None if w is None else _need(w, "w", _F32, (T, s.top_k), dev)
+    if ws is None:
+        raise ValueError("ws: the layer needs a workspace")
     if T == 0:
         return
     _check(load().moe_fp8_layer_forward(layer.ref, px, T, py, pi, pw, _workspace(ws, dev),

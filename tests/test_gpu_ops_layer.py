@@ -256,3 +256,8 @@ def test_refusals():
     assert e.value.status == 3
     with pytest.raises(ValueError):
         moe_ops.moe_fp8_layer_forward(L.handle, x[:4, :32], 4, torch.empty_like(x[:4]), ws)
+    for missing in (dict(x=None), dict(y=None), dict(ws=None)):
+        a = dict(x=x[:4], y=torch.empty_like(x[:4]), ws=ws)
+        a.update(missing)
+        with pytest.raises(ValueError):
+            moe_ops.moe_fp8_layer_forward(L.handle, a["x"], 4, a["y"], a["ws"])

@@ -176,6 +176,11 @@ def test_binding_refuses_host_tensors_and_wrong_types(lib):
         moe_ops.make_fp8_mat(w, w)
     with pytest.raises(ValueError):
         moe_ops.moe_fp8_quant(w.bfloat16(), w, w)
+    for f in (moe_ops._need, lambda *a: moe_ops._rows(*a, {})):
+        with pytest.raises(ValueError, match="expected a tensor"):
+            f(None, "x", (torch.bfloat16,), (4, 64), -1)
+    with pytest.raises(ValueError):
+        moe_ops.make_fp8_mat(w.to(torch.float8_e4m3fn), None)
 
 
 def test_binding_takes_pitched_rows_and_refuses_overlapping_ones():
