@@ -25,8 +25,8 @@
 // the way, 8 tokens of 512 experts (d 2048, ffn 512): all 16 warps on each unit
 // by columns, added up between block barriers, 100 us; the same from rings of
 // bulk copies 85 us; one warp per unit with rotating registers (loops unrolled
-// four times) 79 us; this form 70 us (gate/up at 5 TB/s, down at 3.7 TB/s), and 25
-// us for one token.
+// four times) 79 us; this form 67 us (gate/up 29 us at 4.6 TB/s,
+// down 20 us at 3.6 TB/s), and 24 us for one token.
 //
 // Rows 0-7 of the 16 of mma.sync m16n8k32 are gate rows and rows 8-15 the up
 // rows of the same channels, which leaves gate and up of one channel and token in
