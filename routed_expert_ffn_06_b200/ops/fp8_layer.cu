@@ -25,8 +25,8 @@
 // the way, 8 tokens of 512 experts (d 2048, ffn 512): all 16 warps on each unit
 // by columns, added up between block barriers, 100 us; the same from rings of
 // bulk copies 85 us; one warp per unit with rotating registers (loops unrolled
-// four times) 79 us; this form 67 us (gate/up 29 us at 4.6 TB/s,
-// down 20 us at 3.6 TB/s), and 24 us for one token.
+// four times) 79 us; this form 64 us (gate/up 27 us at 5 TB/s, down
+// 20 us at 3.6 TB/s), and 24 us for one token.
 //
 // Rows 0-7 of the 16 of mma.sync m16n8k32 are gate rows and rows 8-15 the up
 // rows of the same channels, which leaves gate and up of one channel and token in
@@ -226,8 +226,11 @@ __device__ __noinline__ void fl_topk(const uint32_t* keys, const float* row, int
 }
 
 // 16 bytes (or, with on = false, zeros) to this lane's place of a ring slot.
+// The L2 is asked for 256 bytes of a row at a time, the next column block with this
+// one: the streams of all warps lie in tens of thousands of rows, and half as many
+// visits to each take 8 tokens from 67.2 to 64.4 us.
 __device__ __forceinline__ void fl_copy16(unsigned char* dst, const void* src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
                "r"(on ? 16u : 0u)
                : "memory");
 }
