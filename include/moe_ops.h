@@ -175,7 +175,8 @@ size_t moe_fp8_layer_workspace_bytes(const moe_fp8_layer* layer, int32_t max_tok
  * are not quantised: a token's columns enter the gate/up products exactly, except
  * that in each 128 columns values below 2^-13 of the largest are off by up to
  * 2^-21 of it; the hidden values, with the routing weight folded in, enter the
- * down product in fp16 after a power-of-two scale per expert and token.  Sums
+ * down product as two fp16 terms after a power-of-two scale per expert and token:
+ * 22 bits of each, or an error below 2^-39 of the token's largest.  Sums
  * are fp32.  An infinity or NaN in a token makes its row of y NaN; one in an
  * expert's weights reaches only the tokens that selected the expert.
  *  x: dev bf16 [T][d]; y: dev bf16 [T][d], not x; both 16-byte aligned.

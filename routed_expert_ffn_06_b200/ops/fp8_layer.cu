@@ -25,8 +25,8 @@
 // the way, 8 tokens of 512 experts (d 2048, ffn 512): all 16 warps on each unit
 // by columns, added up between block barriers, 100 us; the same from rings of
 // bulk copies 85 us; one warp per unit with rotating registers (loops unrolled
-// four times) 79 us; this form 64 us (gate/up 27 us at 5 TB/s, down
-// 20 us at 3.6 TB/s), and 24 us for one token.
+// four times) 79 us; this form 67 us (gate/up 27 us at 5 TB/s, down
+// 23 us at 3.2 TB/s), and 25 us for one token.
 //
 // Rows 0-7 of the 16 of mma.sync m16n8k32 are gate rows and rows 8-15 the up
 // rows of the same channels, which leaves gate and up of one channel and token in
@@ -41,9 +41,11 @@
 // first term holds the upper 4 bits of a value's 8, the second, times 16, the
 // rest: exact down to 2^-13 of the block's largest, and off by at most 2^-21 of
 // it below. Phase 4 multiplies fp16: the codes convert exactly, and the hidden
-// values (fp32 in memory) are scaled by a power of two per expert and token that
-// brings the largest to 2^14..2^15, so that each keeps 11 bits or an error below
-// 2^-39 of the largest.
+// values (fp32 in memory), scaled by a power of two per expert and token that
+// brings the largest to 2^14..2^15, are the sum of two fp16 terms, so that each
+// keeps 22 bits or an error below 2^-39 of the largest.  (The first term alone, 11
+// bits, takes 64 us in place of 67 and is off by more than everything else in the
+// layer together.)
 #include "ops.h"
 #include "select.cuh"
 #include "tc.cuh"
@@ -707,9 +709,14 @@ __global__ void __launch_bounds__(FL_THREADS, 1) fp8_layer_kernel(FlArgs a) {
             uint32_t a01, a23, c01, c23;
             dequant4h(word(v0, s), a01, a23);
             dequant4h(word(v1, s), c01, c23);
-            const float4 hv = h[x][4 * j + s];
-            mma_half(acc[j], a01, c01, a23, c23, h2_as_u32(__floats2half2_rn(hv.x * f, hv.y * f)),
-                     h2_as_u32(__floats2half2_rn(hv.z * f, hv.w * f)));
+            const float4 hv = h[x][4 * j + s];   // times f, as two fp16 terms
+            const float2 v01 = make_float2(hv.x * f, hv.y * f), v23 = make_float2(hv.z * f, hv.w * f);
+            const __half2 p01 = __float22half2_rn(v01), p23 = __float22half2_rn(v23);
+            mma_half(acc[j], a01, c01, a23, c23, h2_as_u32(p01), h2_as_u32(p23));
+            const float2 q01 = __half22float2(p01), q23 = __half22float2(p23);
+            mma_half(acc[j], a01, c01, a23, c23,
+                     h2_as_u32(__floats2half2_rn(v01.x - q01.x, v01.y - q01.y)),
+                     h2_as_u32(__floats2half2_rn(v23.x - q23.x, v23.y - q23.y)));
           }
         }
 #pragma unroll
