@@ -93,14 +93,15 @@ __device__ __forceinline__ uint32_t load_acquire(const uint32_t* p) {
   return v;
 }
 
-// Wait until *p reaches n; bounded like every wait of the library.
+// Wait until *p reaches n (by signed distance: a counter that starts below zero has
+// not reached it); bounded like every wait of the library.
 __device__ __forceinline__ bool grid_wait(const uint32_t* p, uint32_t n, Control* ctl,
                                           uint32_t where) {
-  if (load_acquire(p) >= n) return true;
+  if ((int32_t)(load_acquire(p) - n) >= 0) return true;
   const unsigned long long t0 = globaltimer_ns();
   unsigned long long limit = 0;
   for (;;) {
-    if (load_acquire(p) >= n) return true;
+    if ((int32_t)(load_acquire(p) - n) >= 0) return true;
     const unsigned long long el = globaltimer_ns() - t0;
     if (el > kWaitFloorNs) {
       if (limit == 0) {
