@@ -36,7 +36,8 @@ struct Control {
   uint32_t wait_limit_us;  // bounded-wait limit in microseconds; 0: kWaitLimitNs
   uint32_t err_where;      // first failing site (debug aid)
   uint32_t debug_withhold; // test switch (kWithhold*), 0: off
-  uint32_t pad[58];
+  uint32_t pad[57];
+  uint32_t withhold_ops;   // test switch of the e4m3 products, 0: off
 };
 static_assert(sizeof(Control) == 256, "control block is 256 bytes");
 

@@ -145,6 +145,14 @@ __device__ __forceinline__ void fg_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+// Test switch: the role `who` of block 0 issues nothing, so that the others' waits
+// for it run out.
+constexpr uint32_t kHoldMma = 1u, kHoldLoads = 2u;
+__device__ __forceinline__ bool fg_held(const Control* ctl, uint32_t who) {
+  return ctl && blockIdx.x == 0 &&
+         *reinterpret_cast<const volatile uint32_t*>(&ctl->withhold_ops) == who;
+}
+
 // acc += s * p on a pair of floats.
 __device__ __forceinline__ void fma2(float2& acc, float2 p, float2 s) {
   unsigned long long a = *reinterpret_cast<unsigned long long*>(&acc);
@@ -347,7 +355,8 @@ __global__ void __launch_bounds__(FG_THREADS, 1) fp8_gemm_kernel(
     int s = 0;
     uint32_t ph = 0;
     int fills = 0;          // capped at kStages
-    long long n = 0;
+    long long n = 0;        // fills issued
+    bool live = !fg_held(a.ctl, kHoldLoads);   // until a wait runs out
     FgTile tl = {};
     for (long long t = blockIdx.x; fg_tile(t, a, BN, rows, first, &tl);
          t += gridDim.x) {
@@ -357,11 +366,12 @@ __global__ void __launch_bounds__(FG_THREADS, 1) fp8_gemm_kernel(
       const uint32_t bytes = ((pieces ? pieces * 32 : FG_BM) + BN) * FG_BK;
       for (int kb = 0; kb < KB; kb += KBS) {
         if (fills == C::kStages) {
-          pipe_wait(&empty[s], ph ^ 1u, a.ctl, 0x401, gave_up);
+          live &= pipe_wait(&empty[s], ph ^ 1u, a.ctl, 0x401, gave_up);
         } else {
           ++fills;
         }
-        if (elected) {
+        if (elected && live) {
+          ++n;
           unsigned char* st = smem + s * C::kStage;
           const int nk = min(KBS, KB - kb);
           mbar_arrive_expect_tx(&full[s], nk * bytes);
@@ -379,35 +389,32 @@ __global__ void __launch_bounds__(FG_THREADS, 1) fp8_gemm_kernel(
             }
           }
         }
-        ++n;
         if (++s == C::kStages) {
           s = 0;
           ph ^= 1u;
         }
       }
     }
-    // the newest phase of each stage may be unconsumed: its copies land first
-    for (long long j = n - fills; j < n; ++j)
-      pipe_wait(&full[j % C::kStages], (uint32_t)(j / C::kStages) & 1u, a.ctl, 0x402, gave_up);
-    pipe_drain(gave_up);
+    if (elected) pipe_drain(full, C::kStages, n, a.ctl, 0x402);
   } else if (warp == 1) {
     // kind::f8f6f4: e4m3 A and B (format 0), fp32 D, both K-major
     const uint32_t idesc = idesc_f16_f32(FG_BM, BN);
     const uint64_t desc0 = sw128_kmajor_desc(smem_u32(smem));
     int s = 0, as = 0, used = 0;     // used: accumulator groups handed out, capped at kGroups
     uint32_t ph = 0, aph = 0;
+    bool live = !fg_held(a.ctl, kHoldMma);   // until a wait runs out
     FgTile tl = {};
     for (long long t = blockIdx.x; fg_tile(t, a, BN, rows, first, &tl);
          t += gridDim.x) {
       for (int kb = 0; kb < KB; kb += KBS) {
         if (used == C::kGroups) {
-          pipe_wait(&acce[as], aph ^ 1u, a.ctl, 0x403, gave_up);
+          live &= pipe_wait(&acce[as], aph ^ 1u, a.ctl, 0x403, gave_up);
         } else {
           ++used;
         }
-        pipe_wait(&full[s], ph, a.ctl, 0x404, gave_up);
+        live &= pipe_wait(&full[s], ph, a.ctl, 0x404, gave_up);
         tc_fence_after();
-        if (elected) {
+        if (elected && live) {
           const uint64_t st = desc0 + (uint64_t)(s * (C::kStage >> 4));
           const uint32_t d = tmem + (uint32_t)(as * KBS * BN);
           const int nk = min(KBS, KB - kb);
@@ -599,6 +606,7 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
       uint32_t ph = 0;
       int fills = 0;
       long long n = 0;
+      bool live = !fg_held(a.ctl, kHoldLoads);
       FgTile tl = {};
       for (long long t = blockIdx.x; fg_tile(t, a, BN, rows, first, &tl); t += gridDim.x) {
         const int nrow = min(FG_BM, tl.m_end - tl.m0), pieces = nrow > 96 ? 0 : (nrow + 31) / 32;
@@ -606,11 +614,12 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
         const int wrow = tl.g * a.N + tl.n0;
         for (int kb = 0; kb < KB; ++kb) {
           if (fills == stages) {
-            pipe_wait(&empty[s], ph ^ 1u, a.ctl, 0x411, gave_up);
+            live &= pipe_wait(&empty[s], ph ^ 1u, a.ctl, 0x411, gave_up);
           } else {
             ++fills;
           }
-          if (elected) {
+          if (elected && live) {
+            ++n;
             unsigned char* st = smem + s * FW_STAGE;
             mbar_arrive_expect_tx(&full[s], bytes);
             if (pieces == 0) {
@@ -621,33 +630,30 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
             }
             fg_tma_2d(st + FW_HALF, &mp.w, kb * FG_BK, wrow, &full[s]);
           }
-          ++n;
           if (++s == stages) {
             s = 0;
             ph ^= 1u;
           }
         }
       }
-      // the newest phase of each stage may be unconsumed: its copies land first
-      for (long long j = n - fills; j < n; ++j)
-        pipe_wait(&full[j % stages], (uint32_t)(j / stages) & 1u, a.ctl, 0x412, gave_up);
-      pipe_drain(gave_up);
+      if (elected) pipe_drain(full, stages, n, a.ctl, 0x412);
     } else if (warp == 1) {
       const uint32_t idesc = idesc_f16_f32(FG_BM, BN);
       const uint64_t desc0 = sw128_kmajor_desc(smem_u32(smem));
       int s = 0, as = 0, used = 0;
       uint32_t ph = 0, aph = 0;
+      bool live = !fg_held(a.ctl, kHoldMma);
       FgTile tl = {};
       for (long long t = blockIdx.x; fg_tile(t, a, BN, rows, first, &tl); t += gridDim.x) {
         for (int kb = 0; kb < KB; ++kb) {
-          pipe_wait(&full[s], ph, a.ctl, 0x414, gave_up);
+          live &= pipe_wait(&full[s], ph, a.ctl, 0x414, gave_up);
           if (used == FW_SLOTS) {
-            pipe_wait(&acce[as], aph ^ 1u, a.ctl, 0x413, gave_up);
+            live &= pipe_wait(&acce[as], aph ^ 1u, a.ctl, 0x413, gave_up);
           } else {
             ++used;
           }
           tc_fence_after();
-          if (elected) {
+          if (elected && live) {
             const uint64_t ad = desc0 + (uint64_t)(s * (FW_STAGE >> 4)), bd = ad + (FW_HALF >> 4);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
