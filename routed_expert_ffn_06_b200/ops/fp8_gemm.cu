@@ -480,6 +480,7 @@ __global__ void __launch_bounds__(FG_THREADS, 1) fp8_gemm_kernel(
           sw_n[j] = more ? sw[kb + KBS + j] : 0.f;
         }
         pipe_wait(&accf[as], aph, a.ctl, 0x406, gave_up);
+        __syncwarp();      // the TMEM loads are the whole warp's
         if (!idle) {
           tc_fence_after();
           const uint32_t base = lane_base + (uint32_t)(as * KBS * BN);
@@ -701,6 +702,7 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
           sw_n = sw[kb + 1];
         }
         pipe_wait(&accf[as], aph, a.ctl, 0x416, gave_up);
+        __syncwarp();      // the TMEM loads are the whole warp's
         if (!idle) {
           tc_fence_after();
           const uint32_t base = lane_base + (uint32_t)(as * BN);
