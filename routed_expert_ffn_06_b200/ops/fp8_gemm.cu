@@ -808,20 +808,24 @@ bool fg_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uin
 
 template <int BN, int AR>
 cudaError_t fg_launch(const GemmArgs& a, long long tiles, cudaStream_t st) {
+  // before the maps: this call makes the device's context current to a thread that
+  // has made none yet, and the driver encodes no map without one
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(fp8_gemm_kernel<BN, AR>),
+                                   kMaxSmem);
+  if (e != cudaSuccess) return e;
   FgMaps mp = {};
   if ((AR == FG_BM && !fg_map(&mp.a, a.a, (uint64_t)a.K, (uint64_t)a.M, FG_BM)) ||
       !fg_map(&mp.a32, a.a, (uint64_t)a.K, (uint64_t)a.M, 32) ||
       !fg_map(&mp.w, a.w, (uint64_t)a.K, (uint64_t)a.N * a.G, BN))
     return cudaErrorInvalidValue;
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(fp8_gemm_kernel<BN, AR>),
-                                   kMaxSmem);
-  if (e != cudaSuccess) return e;
   const long long grid = tiles < sm_count() ? tiles : sm_count();
   return launch_pdl(fp8_gemm_kernel<BN, AR>, dim3((unsigned)grid), dim3(FG_THREADS),
                     FgCfg<BN, AR>::smem(a.G), st, a, mp);
 }
 
 cudaError_t fg_launch_wide(const GemmArgs& a, long long tiles, cudaStream_t st) {
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(fp8_gemm_wide_kernel), kMaxSmem);
+  if (e != cudaSuccess) return e;
   FgMaps mp = {};
   if (!fg_map(&mp.a, a.a, (uint64_t)a.K, (uint64_t)a.M, FG_BM) ||
       !fg_map(&mp.a32, a.a, (uint64_t)a.K, (uint64_t)a.M, 32) ||
@@ -838,14 +842,12 @@ cudaError_t fg_launch_wide(const GemmArgs& a, long long tiles, cudaStream_t st) 
   }
   // a block launched with fewer registers than the split hands out would wait for ever
   cudaFuncAttributes at;
-  cudaError_t e = cudaFuncGetAttributes(&at, reinterpret_cast<const void*>(fp8_gemm_wide_kernel));
+  e = cudaFuncGetAttributes(&at, reinterpret_cast<const void*>(fp8_gemm_wide_kernel));
   if (e != cudaSuccess) return e;
   if (at.numRegs != FW_REGS) return cudaErrorInvalidConfiguration;
   // the offsets of very many groups take the place of one stage
   const int stages = fw_smem(FW_MAX_STAGES, a.G) <= kMaxSmem ? FW_MAX_STAGES : FW_MAX_STAGES - 1;
   const size_t sm = fw_smem(stages, a.G);
-  e = allow_smem(reinterpret_cast<const void*>(fp8_gemm_wide_kernel), kMaxSmem);
-  if (e != cudaSuccess) return e;
   const long long grid = tiles < sm_count() ? tiles : sm_count();
   return launch_pdl(fp8_gemm_wide_kernel, dim3((unsigned)grid), dim3(FW_THREADS), sm, st, a, stages,
                     mp);
