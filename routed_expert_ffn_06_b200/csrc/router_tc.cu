@@ -199,14 +199,16 @@ cudaError_t launch_router_tc(const LayerDev& L, const uint16_t* x, int T, float*
     e = launch_split_router(L.Wr, L.E, L.d, hi, lo, st);
     if (e != cudaSuccess) return e;
   }
+  // before the maps: this call makes the device's context current to a thread that
+  // has made none yet, and the driver encodes no map without one
+  const size_t sm = router_tc_smem();
+  e = cudaFuncSetAttribute(router_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+  if (e != cudaSuccess) return e;
   RtMaps mp;
   if (!make_map_b16(&mp.hi, hi, (uint64_t)L.d, (uint64_t)L.E) ||
       !make_map_b16(&mp.lo, lo, (uint64_t)L.d, (uint64_t)L.E) ||
       !make_map_b16(&mp.x, x, (uint64_t)L.d, (uint64_t)T))
     return cudaErrorInvalidValue;
-  const size_t sm = router_tc_smem();
-  e = cudaFuncSetAttribute(router_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
-  if (e != cudaSuccess) return e;
   dim3 grid((L.E + 127) / 128, (T + 127) / 128);
   return launch_pdl(router_tc_kernel, grid, dim3(RT_THREADS), sm, st,
                     static_cast<const float*>(L.bias), L.E, T, L.d, logits, ctl, mp);
