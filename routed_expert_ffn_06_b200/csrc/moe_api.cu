@@ -3,6 +3,8 @@
 #include <cuda_runtime.h>
 #include <stdio.h>
 
+#include <atomic>
+
 #include "internal.h"
 
 #define MOE_STR_(x) #x
@@ -17,8 +19,9 @@ size_t prefill_ws_bytes(const LayerDev& L, int T, size_t* parts);
 
 namespace {
 constexpr int kMaxDevices = 64;
-int g_sm_count[kMaxDevices];
-int g_dev_ok[kMaxDevices];  // 0 unknown, 1 ok, -1 not an sm_100 device
+// What is known of a device; written by whichever thread asks first (g_dev_ok last).
+std::atomic<int> g_sm_count[kMaxDevices];
+std::atomic<int> g_dev_ok[kMaxDevices];  // 0 unknown, 1 ok, -1 not an sm_100 device
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
@@ -143,7 +146,7 @@ moe_status preamble(const moe_layer* layer, int32_t T, const void* x, void* ws, 
 int sm_count() {
   int dev = 0;
   cudaGetDevice(&dev);
-  return (dev >= 0 && dev < kMaxDevices && g_sm_count[dev] > 0) ? g_sm_count[dev] : 148;
+  return (dev >= 0 && dev < kMaxDevices && g_sm_count[dev] > 0) ? g_sm_count[dev].load() : 148;
 }
 
 WsLayout ws_layout(const LayerDev& L, int T) {

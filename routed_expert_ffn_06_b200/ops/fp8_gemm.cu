@@ -23,6 +23,8 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
+
 #include "ops.h"
 #include "pipe.cuh"
 #include "tc.cuh"
@@ -780,14 +782,19 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
+// Looked up once; calls of several threads that come first together each look it up
+// and find the same.
 PFN_cuTensorMapEncodeTiled_v12000 fg_encode() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> cached{nullptr};
+  PFN_cuTensorMapEncodeTiled_v12000 fn = cached.load(std::memory_order_acquire);
   if (!fn) {
     cudaDriverEntryPointQueryResult q;
     void* p = nullptr;
     if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
+        q == cudaDriverEntryPointSuccess) {
       fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+      cached.store(fn, std::memory_order_release);
+    }
   }
   return fn;
 }
