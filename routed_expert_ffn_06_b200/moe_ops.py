@@ -161,11 +161,18 @@ class _Handle:
             raise ValueError(f"weights on cuda:{self.dev}, not on the current CUDA device")
 
 
+CONTROL_BYTES = 256     # a workspace's control block, which holds the error word
+
+
 def _workspace(ws, dev):
-    """Address of a workspace: dense bytes on the current device."""
+    """Address of a workspace: dense bytes on the current device, a control block
+    of them at least."""
     if ws is None:
         return None
-    return _need(ws, "ws", (torch.uint8,), getattr(ws, "shape", None), dev)
+    p = _need(ws, "ws", (torch.uint8,), getattr(ws, "shape", None), dev)
+    if ws.numel() < CONTROL_BYTES:
+        raise ValueError(f"ws: {ws.numel()} bytes, expected at least {CONTROL_BYTES}")
+    return p
 
 
 # ------------------------------------------------------------------- norms
