@@ -117,6 +117,15 @@ def _need(t, name, dtypes, shape, dev):
     raise ValueError(f"{name}: not contiguous")
 
 
+def _shape(t, name, form, *ranks):
+    """Shape of a tensor that has one of these numbers of dimensions."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name}: {type(t).__name__}, expected a tensor")
+    if t.dim() not in ranks:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {form}")
+    return t.shape
+
+
 def _rows(t, name, dtypes, shape, dev, pitched):
     """The same for rows that are dense themselves but may have any pitch, which
     is noted in the dict `pitched` where it is not the row's length."""
@@ -230,10 +239,9 @@ def moe_norm_block(n: _Handle, x, y, gate, T: int, x_out=None, h=None, codes=Non
 def make_fp8_mat(codes, scales) -> _Handle:
     """A weight matrix [N, K], or one per group [G, N, K], with its block
     scales [(G,) ceil(N/128), ceil(K/128)]."""
-    if codes.dim() not in (2, 3):
-        raise ValueError("codes: [N, K] or [G, N, K]")
-    lead, (N, K), dev = tuple(codes.shape[:-2]), codes.shape[-2:], _current()
-    _need(codes, "codes", _E4M3, codes.shape, dev)
+    shape, dev = _shape(codes, "codes", "[N, K] or [G, N, K]", 2, 3), _current()
+    lead, (N, K) = tuple(shape[:-2]), shape[-2:]
+    _need(codes, "codes", _E4M3, shape, dev)
     _need(scales, "scales", _F32, lead + (_blocks(N), _blocks(K)), dev)
     return _Handle(moe_fp8_mat(N, K, lead[0] if lead else 1, _ptr(codes), _ptr(scales)), codes,
                    scales)
@@ -241,9 +249,7 @@ def make_fp8_mat(codes, scales) -> _Handle:
 
 def moe_fp8_quant(x, codes, scales, stream=None) -> None:
     """bf16 rows [T, d] to e4m3 codes [T, d] and scales [T, ceil(d/128)]."""
-    if x.dim() != 2:
-        raise ValueError("x: [T, d]")
-    (T, d), dev = x.shape, _current()
+    (T, d), dev = _shape(x, "x", "[T, d]", 2), _current()
     pitched = {}
     px = _rows(x, "x", _BF16, x.shape, dev, pitched)
     pc = _need(codes, "codes", _E4M3, (T, d), dev)
@@ -293,9 +299,9 @@ def make_fp8_layer(top_k: int, router_w, router_bias, gate_up, gate_up_scales, d
     [E] or None, gate_up e4m3 [E, 2, F, d] (gate rows, then up rows), down
     [E, d, F], the shared expert [2, Fs, d] and [d, Fs] or None, each with its
     scales per 128 x 128 block."""
-    E, d = router_w.shape
-    F = gate_up.shape[-2]
-    Fs = 0 if shared_gate_up is None else shared_gate_up.shape[-2]
+    E, d = _shape(router_w, "router_w", "[E, d]", 2)
+    F = _shape(gate_up, "gate_up", "[E, 2, F, d]", 4)[-2]
+    Fs = 0 if shared_gate_up is None else _shape(shared_gate_up, "shared_gate_up", "[2, Fs, d]", 3)[-2]
     kd, kf, ks, dev = _blocks(d), _blocks(F), _blocks(Fs), _current()
     _need(router_w, "router_w", _F32, (E, d), dev)
     if router_bias is not None:
