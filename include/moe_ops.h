@@ -108,7 +108,8 @@ typedef struct moe_fp8_mat_s {
 /* bf16 rows to codes and scales, as moe_norm_block writes them.
  *  x: dev bf16 [T][d], rows ld elements apart (0 = d; >= d, a multiple of 8);
  *  d a multiple of 8, 8 <= d <= 65536; codes: dev [T][d], 8-byte aligned;
- *  scales: dev fp32 [T][ceil(d/128)].  x: 16-byte aligned.  T = 0 enqueues nothing. */
+ *  scales: dev fp32 [T][ceil(d/128)].  x: 16-byte aligned.  Outputs may not overlap
+ *  x or each other.  T = 0 enqueues nothing. */
 moe_status moe_fp8_quant(const void* x, int64_t ld, int32_t T, int32_t d, uint8_t* codes,
                          float* scales, void* stream);
 
@@ -118,7 +119,8 @@ moe_status moe_fp8_quant(const void* x, int64_t ld, int32_t T, int32_t d, uint8_
  * fp32, one rounding to bf16.
  *  a: dev e4m3 [M][K] (dense rows), 16-byte aligned; a_scales: dev fp32
  *  [M][ceil(K/128)]; c: dev bf16 [M][N] (dense rows), 2-byte aligned (16-byte
- *  aligned with N a multiple of 8 stores faster).  w->groups must be 1.
+ *  aligned with N a multiple of 8 stores faster), which may not overlap a or
+ *  a_scales.  w->groups must be 1.
  *  A NaN code or scale in a row of a, or of the weights, stays in that row, or
  *  column, of c.  M = 0 enqueues nothing.
  *  ws_or_null: a workspace of at least 256 bytes, zeroed once with
@@ -179,7 +181,8 @@ size_t moe_fp8_layer_workspace_bytes(const moe_fp8_layer* layer, int32_t max_tok
  * 22 bits of each, or an error below 2^-39 of the token's largest.  Sums
  * are fp32.  An infinity or NaN in a token makes its row of y NaN; one in an
  * expert's weights reaches only the tokens that selected the expert.
- *  x: dev bf16 [T][d]; y: dev bf16 [T][d], not x; both 16-byte aligned.
+ *  x: dev bf16 [T][d]; y: dev bf16 [T][d], which may not overlap x; both 16-byte
+ *  aligned.
  *  ids_or_null: dev int32 [T][k]; w_or_null: dev fp32 [T][k]: the routing,
  *  written when non-NULL.
  * Windows of up to 8 tokens run as one kernel over all SMs, whose blocks wait

@@ -10,6 +10,12 @@ namespace {
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+// Two ranges of bytes have one in common.
+bool overlap(const void* p, size_t np, const void* q, size_t nq) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a < b + nq && b < a + np && np && nq;
+}
+
 moe_status from_cuda(cudaError_t e) {
   if (e == cudaSuccess) return MOE_OK;
   cudaGetLastError();
@@ -41,6 +47,10 @@ moe_status gemm(const moe_fp8_mat* w, const uint8_t* a, const float* a_scales, i
   if (!aligned(a, 16) || !aligned(a_scales, 4) || !aligned(c, 2) || !aligned(offsets, 4) ||
       !aligned(ws, 256))
     return MOE_ERR_MISALIGNED;
+  const size_t cb = (size_t)M * w->n * 2;
+  if (overlap(c, cb, a, (size_t)M * w->k) ||
+      overlap(c, cb, a_scales, (size_t)M * blocks128(w->k) * 4))
+    return MOE_ERR_INVALID_ARG;
   if ((s = check_device()) != MOE_OK) return s;
   if (M == 0) return MOE_OK;
   GemmArgs g;
@@ -213,6 +223,7 @@ moe_status moe_fp8_layer_forward(const moe_fp8_layer* layer, const void* x_bf16,
       !aligned(ids_or_null, 4) || !aligned(w_or_null, 4))
     return MOE_ERR_MISALIGNED;
   const Fp8LayerDev L = to_dev(layer);
+  if (overlap(x_bf16, (size_t)T * L.d * 2, y_bf16, (size_t)T * L.d * 2)) return MOE_ERR_INVALID_ARG;
   if (ws_bytes < fp8_layer_ws_bytes(L)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   if ((s = check_device()) != MOE_OK) return s;
   for (int t0 = 0; t0 < T; t0 += kFp8Window) {
