@@ -77,9 +77,9 @@ typedef struct moe_norm_s {
  *  h_or_null: dev bf16 [T][d];
  *  codes_or_null, scales_or_null (both or neither): h in e4m3, dev uint8
  *    [T][d] (dense rows) and dev fp32 [T][ceil(d/128)]: for each 128 columns
- *    scale = max|h| / 448 and code = e4m3(h / scale), nearest, ties to even;
- *    a block of zeros has scale 0 and codes 0.  The codes are taken from h
- *    before its rounding to bf16.
+ *    scale = max|h| / 448 and code = e4m3(h / scale), every step to nearest, ties
+ *    to even (the quotients in fp32); a block of zeros has scale 0 and codes 0.
+ *    The codes are taken from h before its rounding to bf16.
  * x: dev [T][d] of the stream's type; y_or_null: dev bf16 [T][d].
  * x_out may be x itself (same pitch), and h may be y itself (same pitch);
  * otherwise outputs may not overlap inputs or each other.

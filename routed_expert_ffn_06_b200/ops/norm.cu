@@ -96,14 +96,21 @@ __device__ __forceinline__ void quant8(const float2 (&v)[4], bool live, uint8_t*
   if (!live) top = 0.f;
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) top = max3_abs(top, __shfl_xor_sync(0xffffffffu, top, o), 0.f);
-  const float s = top * (1.f / kE4m3Max);
   if (!live) return;
-  // one division for the block; v / s would overflow it below about 1e-36
-  const float2 inv = both(kE4m3Max / fmaxf(top, 1e-30f));
+  // Both quotients are rounded as by a division: a product with the reciprocal, and
+  // what it leaves of the dividend (exact, by fma) divided again.
+  float s = top * (1.f / kE4m3Max);
+  s = fmaf(fmaf(-s, kE4m3Max, top), 1.f / kE4m3Max, s);
   float2 q[4];
+  if (top > 1e-24f && top < 1e38f) {
+    const float inv = __frcp_rn(s);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) q[j] = mul2(v[j], inv);
-  if (top < 1e-30f) {
+    for (int j = 0; j < 4; ++j) {
+      q[j] = mul2(v[j], both(inv));
+      q[j] = fma2(fma2(q[j], both(-s), v[j]), both(inv), q[j]);
+    }
+  } else {   // zeros, values whose remainders underflow, infinities, NaN
+    s = top / kE4m3Max;
 #pragma unroll
     for (int j = 0; j < 4; ++j) q[j] = s != 0.f ? make_float2(v[j].x / s, v[j].y / s) : v[j];
   }
