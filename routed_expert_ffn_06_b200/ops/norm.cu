@@ -8,9 +8,9 @@
 //
 // One pass over memory: a row stays in registers between the loads and the
 // stores, so every byte is read once and written once.  Many rows are bound by
-// HBM without a gate and a quantiser (8192 x 2048: 6.0 TB/s) and by the
-// instructions issued with them (5.2 TB/s); one row by its launch and two
-// dependent reductions.
+// HBM with the second norm alone (8192 x 2048: 22.5 us, 6.0 TB/s), by the instructions
+// issued with a post norm (27.0 us, 5.0 TB/s) and with a gate and the quantiser as
+// well (35.4 us, 5.2 TB/s); one row by its launch and two dependent reductions.
 // A thread owns chunks of 8 consecutive channels (16-byte accesses in bf16).
 // Rows of up to 512 channels take one warp each (no block barrier); wider rows
 // take a block each, of as many threads as chunks (measured: 777 x 1000 channels
@@ -131,16 +131,19 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
   return warp_sum(lane < nw ? red[lane] : 0.f);
 }
 
-// 1 / (1 + e^-x): the fast exponential and reciprocal are off by |x| 2^-24 and a
-// few last bits, and exact division and exp took a third of the kernel's time.
+// 1 / (1 + e^-x): the fast exponential is off by 2 + 1.2 |x| last bits and the fast
+// division by 2, which is 2^-21 of 1 at most; exact division and exp took a third
+// of the kernel's time.
 __device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
 
 constexpr int kWarpRows = 4;   // rows (warps) of a block when a row takes one warp
 
-// 32 registers keep two blocks of 1024 threads, or eight of 256, on an SM: without
-// the bound the pairs take 37, and 2048 x 8192 channels 51 us in place of 40.  With
-// single floats 8192 x 2048 takes 37.1 us in place of 35.5, 30,000 x 512 22.7 in
-// place of 22.0, 2048 x 8192 38.6.
+// 32 registers keep two blocks of 1024 threads, or eight of 256, on an SM, and spill
+// 16 bytes a thread; without the bound one token of 2048 channels takes 2.29 us in
+// place of 2.13, 8192 x 1024 17.7 in place of 17.4, and the rows bound by issue gain:
+// 8192 x 2048 34.6 in place of 35.4, 2048 x 8192 36.3 in place of 37.6.  Pairs in
+// place of single floats took 8192 x 2048 from 37.1 to 35.5 us and 30,000 x 512 from
+// 22.7 to 22.0.
 template <bool F32, bool WARP_ROW, int CH>
 __global__ void __launch_bounds__(WARP_ROW ? 32 * kWarpRows : 1024, WARP_ROW ? 1 : 2) norm_block_kernel(NormArgs a) {
   __shared__ float red[2][32];
