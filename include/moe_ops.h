@@ -143,6 +143,11 @@ moe_status moe_fp8_gemm_grouped(const moe_fp8_mat* w, const uint8_t* a, const fl
                                 int32_t M, const int32_t* offsets, void* c_bf16, void* ws_or_null,
                                 void* stream);
 
+/* The kernel that a product of M >= 1 rows takes: plan[0] columns of a tile, plan[1]
+ * rows of a staged for it, plan[2] stages of the operand ring.  Host only; for the
+ * current device's SMs, or 148 where no call of the library has asked for them yet. */
+moe_status moe_fp8_gemm_plan(const moe_fp8_mat* w, int32_t M, int32_t grouped, int32_t plan[3]);
+
 /* ------------------------------------------------------------------ layer */
 
 /* One MoE layer with e4m3 experts.  A host struct, read only during the call. */

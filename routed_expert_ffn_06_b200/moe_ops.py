@@ -36,7 +36,7 @@ GATES = {"none": 0, "token": 1, "channel": 2, "full": 3}
 FP8_LAYER_MAX_T = 32
 
 EXPORTS = ["moe_norm_block", "moe_fp8_quant", "moe_fp8_gemm", "moe_fp8_gemm_grouped",
-           "moe_fp8_layer_workspace_bytes", "moe_fp8_layer_forward"]
+           "moe_fp8_gemm_plan", "moe_fp8_layer_workspace_bytes", "moe_fp8_layer_forward"]
 
 
 class moe_norm(ctypes.Structure):
@@ -79,6 +79,7 @@ def load() -> ctypes.CDLL:
             ("moe_fp8_quant", [vp, i64, i32, i32, vp, vp, vp]),
             ("moe_fp8_gemm", [vp, vp, vp, i32, vp, vp, vp]),
             ("moe_fp8_gemm_grouped", [vp, vp, vp, i32, vp, vp, vp, vp]),
+            ("moe_fp8_gemm_plan", [vp, i32, i32, vp]),
             ("moe_fp8_layer_forward", [vp, vp, i32, vp, vp, vp, vp, sz, vp])]:
         f = getattr(L, name)
         f.restype, f.argtypes = st, args
@@ -289,6 +290,13 @@ def moe_fp8_gemm_grouped(w: _Handle, a, a_scales, M: int, offsets, c, ws=None, s
     _check(load().moe_fp8_gemm_grouped(w.ref, pa, psa, M, po, pc, _workspace(ws, dev),
                                        _stream(stream, dev)),
            "moe_fp8_gemm_grouped")
+
+
+def moe_fp8_gemm_plan(w: _Handle, M: int, grouped: bool = False):
+    """The kernel a product takes: (tile columns, rows of a staged, ring stages)."""
+    plan = (ctypes.c_int32 * 3)()
+    _check(load().moe_fp8_gemm_plan(w.ref, M, int(grouped), plan), "moe_fp8_gemm_plan")
+    return tuple(plan)
 
 
 # ------------------------------------------------------------------- layer

@@ -553,6 +553,11 @@ __host__ __device__ constexpr size_t fw_smem(int stages, int G) {
          (2 * FW_MAX_STAGES + 2 * FW_SLOTS + 1) * 8 + 16 + (size_t)(2 * G + 2) * 4;
 }
 
+// From 241 groups on their offsets take the place of one stage.
+int fw_stages(int G) {
+  return fw_smem(FW_MAX_STAGES, G) <= kMaxSmem ? FW_MAX_STAGES : FW_MAX_STAGES - 1;
+}
+
 __global__ void __launch_bounds__(FW_THREADS, 1)
     fp8_gemm_wide_kernel(GemmArgs a, int stages, const __grid_constant__ FgMaps mp) {
   constexpr int BN = 256;
@@ -830,7 +835,7 @@ cudaError_t fg_launch(const GemmArgs& a, long long tiles, cudaStream_t st) {
                     FgCfg<BN, AR>::smem(a.G), st, a, mp);
 }
 
-cudaError_t fg_launch_wide(const GemmArgs& a, long long tiles, cudaStream_t st) {
+cudaError_t fg_launch_wide(const GemmArgs& a, const GemmPlan& p, cudaStream_t st) {
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(fp8_gemm_wide_kernel), kMaxSmem);
   if (e != cudaSuccess) return e;
   FgMaps mp = {};
@@ -852,12 +857,9 @@ cudaError_t fg_launch_wide(const GemmArgs& a, long long tiles, cudaStream_t st) 
   e = cudaFuncGetAttributes(&at, reinterpret_cast<const void*>(fp8_gemm_wide_kernel));
   if (e != cudaSuccess) return e;
   if (at.numRegs != FW_REGS) return cudaErrorInvalidConfiguration;
-  // the offsets of very many groups take the place of one stage
-  const int stages = fw_smem(FW_MAX_STAGES, a.G) <= kMaxSmem ? FW_MAX_STAGES : FW_MAX_STAGES - 1;
-  const size_t sm = fw_smem(stages, a.G);
-  const long long grid = tiles < sm_count() ? tiles : sm_count();
-  return launch_pdl(fp8_gemm_wide_kernel, dim3((unsigned)grid), dim3(FW_THREADS), sm, st, a, stages,
-                    mp);
+  const long long grid = p.tiles < sm_count() ? p.tiles : sm_count();
+  return launch_pdl(fp8_gemm_wide_kernel, dim3((unsigned)grid), dim3(FW_THREADS),
+                    fw_smem(p.stages, a.G), st, a, p.stages, mp);
 }
 
 }  // namespace
@@ -866,43 +868,50 @@ cudaError_t fg_launch_wide(const GemmArgs& a, long long tiles, cudaStream_t st) 
 // bytes that a block loads per k-block, the rows of A and of W, since that is
 // what bounds it (the L2's rate for wide tiles, HBM's for narrow ones), plus a
 // fixed part.
-cudaError_t launch_fp8_gemm(const GemmArgs& a, cudaStream_t st) {
+GemmPlan plan_fp8_gemm(int M, int N, int G, bool grouped, int sms) {
   // row tiles: the groups hold M rows in all, each at most one partial tile
-  const int groups = a.offsets ? (a.G < a.M ? a.G : a.M) : 1;
-  const long long mt = a.offsets ? a.M / FG_BM + groups : (a.M + FG_BM - 1) / FG_BM;
-  const long long avg = (a.M + groups - 1) / groups;
+  const int groups = grouped ? (G < M ? G : M) : 1;
+  const long long mt = grouped ? M / FG_BM + groups : (M + FG_BM - 1) / FG_BM;
+  const long long avg = groups ? (M + groups - 1) / groups : 0;
   const long long rows = avg >= FG_BM ? FG_BM : (avg + 31) / 32 * 32;
-  const bool few = a.M <= 32;      // no tile has more than 32 rows
-  const int sms = sm_count();
-  long long best = 0, tiles = 0;
-  int bn = 0;
-  for (int b = 128; b >= 16; b >>= 1) {
-    const long long t = mt * ((a.N + b - 1) / b);
+  const bool few = M <= 32;        // no tile has more than 32 rows
+  GemmPlan p = {};
+  long long best = 0;
+  for (int b = few ? 128 : 256; b >= 16; b >>= 1) {
+    const long long t = mt * ((N + b - 1) / b);
     const long long cost = (t + sms - 1) / sms * (rows + b + 32);
-    if (bn == 0 || cost < best) {
+    // (equal cost: the wider, except that 256 has to be better)
+    if (p.bn == 0 || cost < best || (p.bn == 256 && cost == best)) {
       best = cost;
-      bn = b;
-      tiles = t;
+      p.bn = b;
+      p.tiles = t;
     }
   }
-  if (!few) {
-    const long long t = mt * ((a.N + 255) / 256);
-    const long long cost = (t + sms - 1) / sms * (rows + 256 + 32);
-    if (cost < best) return fg_launch_wide(a, t, st);
-  }
-  if (few) {
-    switch (bn) {
-      case 128: return fg_launch<128, 32>(a, tiles, st);
-      case 64: return fg_launch<64, 32>(a, tiles, st);
-      case 32: return fg_launch<32, 32>(a, tiles, st);
-      default: return fg_launch<16, 32>(a, tiles, st);
+  p.a_rows = few ? 32 : FG_BM;
+  p.stages = p.bn == 256   ? fw_stages(G)
+             : p.bn == 128 ? (few ? FgCfg<128, 32>::kStages : FgCfg<128, 128>::kStages)
+             : p.bn == 64  ? (few ? FgCfg<64, 32>::kStages : FgCfg<64, 128>::kStages)
+             : p.bn == 32  ? (few ? FgCfg<32, 32>::kStages : FgCfg<32, 128>::kStages)
+                           : (few ? FgCfg<16, 32>::kStages : FgCfg<16, 128>::kStages);
+  return p;
+}
+
+cudaError_t launch_fp8_gemm(const GemmArgs& a, cudaStream_t st) {
+  const GemmPlan p = plan_fp8_gemm(a.M, a.N, a.G, a.offsets != nullptr, sm_count());
+  if (p.a_rows == 32) {
+    switch (p.bn) {
+      case 128: return fg_launch<128, 32>(a, p.tiles, st);
+      case 64: return fg_launch<64, 32>(a, p.tiles, st);
+      case 32: return fg_launch<32, 32>(a, p.tiles, st);
+      default: return fg_launch<16, 32>(a, p.tiles, st);
     }
   }
-  switch (bn) {
-    case 128: return fg_launch<128, 128>(a, tiles, st);
-    case 64: return fg_launch<64, 128>(a, tiles, st);
-    case 32: return fg_launch<32, 128>(a, tiles, st);
-    default: return fg_launch<16, 128>(a, tiles, st);
+  switch (p.bn) {
+    case 256: return fg_launch_wide(a, p, st);
+    case 128: return fg_launch<128, 128>(a, p.tiles, st);
+    case 64: return fg_launch<64, 128>(a, p.tiles, st);
+    case 32: return fg_launch<32, 128>(a, p.tiles, st);
+    default: return fg_launch<16, 128>(a, p.tiles, st);
   }
 }
 

@@ -52,6 +52,14 @@ struct GemmArgs {
   uint16_t* c;
   Control* ctl;                // or nullptr
 };
+// The kernel a product takes on a device of `sms` SMs.
+struct GemmPlan {
+  int bn;            // columns of a tile
+  int a_rows;        // rows of A staged for a tile
+  int stages;        // of the operand ring
+  long long tiles;   // at most
+};
+GemmPlan plan_fp8_gemm(int M, int N, int G, bool grouped, int sms);
 cudaError_t launch_fp8_gemm(const GemmArgs& a, cudaStream_t st);
 
 struct Fp8LayerDev {

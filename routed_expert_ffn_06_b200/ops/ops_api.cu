@@ -206,6 +206,18 @@ moe_status moe_fp8_gemm_grouped(const moe_fp8_mat* w, const uint8_t* a, const fl
   return gemm(w, a, a_scales, M, offsets, c_bf16, ws_or_null, stream);
 }
 
+moe_status moe_fp8_gemm_plan(const moe_fp8_mat* w, int32_t M, int32_t grouped, int32_t plan[3]) {
+  moe_status s = validate_mat(w);
+  if (s != MOE_OK) return s;
+  if (M < 1 || !plan || (!grouped && w->groups != 1)) return MOE_ERR_INVALID_ARG;
+  if (M > kMaxRows) return MOE_ERR_UNSUPPORTED_SHAPE;
+  const GemmPlan p = plan_fp8_gemm(M, w->n, w->groups, grouped != 0, sm_count());
+  plan[0] = p.bn;
+  plan[1] = p.a_rows;
+  plan[2] = p.stages;
+  return MOE_OK;
+}
+
 size_t moe_fp8_layer_workspace_bytes(const moe_fp8_layer* layer, int32_t max_tokens) {
   if (validate_fp8_layer(layer) != MOE_OK || max_tokens < 0 || max_tokens > MOE_FP8_LAYER_MAX_T)
     return 0;
