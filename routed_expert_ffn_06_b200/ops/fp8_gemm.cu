@@ -526,13 +526,16 @@ __global__ void __launch_bounds__(FG_THREADS, 1) fp8_gemm_kernel(
 }
 
 // ------------------------------------------------------------ wide tiles
-// 128 x 256 tiles for many rows.  The L2 delivers about 68 bytes per cycle and SM
-// (measured), so a k-block's 48 KB take 720 cycles, against 540 of the MMAs; 128 x
-// 128 tiles would need 480 cycles for 270.  Measured: 8192 x 4096 x 2048 in 67 us
-// (2.05 PFLOP/s in a short run), 20,480 rows in 512 groups of 1024 x 2048 in 198 us
-// (5.8 TB/s of weights).  Pairs of SMs on 256 x 256 tiles load 32 KB per SM and
-// k-block, but the hand-overs between two SMs cost what that saves: 65 us for the
-// first, and 420 against 305 us for 81,920 rows in 512 groups.
+// 128 x 256 tiles for many rows.  A k-block takes about 1,130 cycles (8192 x 4096 x
+// 2048: 7 waves of 16 in 77 us at 1.64 GHz under a profiler), of which its MMAs are 540
+// and its 48 KB would be 720 at the 68 bytes per cycle and SM that the L2 was measured
+// to deliver: neither bounds it.  What is left is the round trip of the two accumulators
+// (commit, promotion, hand-back), whose parts were not timed one by one.  Measured in graphs: 8192 x 4096 x 2048 73 us, 20,480
+// rows in 512 groups of 1024 x 2048 204 us, 81,920 rows 300 us; in a long run, under
+// the power cap, the first takes 87 and the last 364 us.  Pairs of SMs on 256 x 256
+// tiles load 32 KB per SM and k-block, but the hand-overs between two SMs cost what
+// that saves (65 against 67 us for the first, 420 against 305 us for the last, on one
+// box).
 //
 // One tcgen05.mma takes all 256 columns: at 128 columns a block's MMAs read A
 // twice and shared memory at 122 bytes per cycle, which nearly halves their rate.
@@ -864,10 +867,24 @@ cudaError_t fg_launch_wide(const GemmArgs& a, const GemmPlan& p, cudaStream_t st
 
 }  // namespace
 
-// The tile width with the least estimated time.  A wave of tiles costs the
-// bytes that a block loads per k-block, the rows of A and of W, since that is
-// what bounds it (the L2's rate for wide tiles, HBM's for narrow ones), plus a
-// fixed part.
+// The tile width with the least estimated time.  The estimate of a wave of tiles is
+// the rows of A and of W that a block loads per k-block and a fixed part: no account of
+// what bounds a kernel, but an order of the widths that measurement bears out.  Times
+// in us by width, * the choice (G: groups):
+//         M      N     K    G     16      32      64     128     256
+//         4   2048  2048          5.0*    4.8     5.2     6.6
+//         4   4096  2048          7.8     5.4*    5.5     6.7
+//         4   8192  2048         12.3     8.3     6.4*    6.9
+//         4  16384  2048         21.5    14.4    10.6     9.0*
+//       100   2048  2048          5.6*    5.7     6.0     7.3    11.2
+//       333   1000  1936          9.8     6.6*    7.6     9.8    13.6
+//       512   4096  2048         25.6    16.4    10.6     8.2*   12.0
+//      1024   4096  2048         47.9    26.4    18.1    14.2    12.5*
+//      8192   4096  2048        359     186     105      84.8    73.9*
+//        20   2048  2048  512    57.3    36.9    28.9    27.7*
+//       640   2048   512  512   349     185     115      85.2    80.1*
+//     5,000   1024  2048  512   766     398     220     191     201*
+//    81,920   1024  2048  512  1362     724     459     361     353*
 GemmPlan plan_fp8_gemm(int M, int N, int G, bool grouped, int sms) {
   // row tiles: the groups hold M rows in all, each at most one partial tile
   const int groups = grouped ? (G < M ? G : M) : 1;

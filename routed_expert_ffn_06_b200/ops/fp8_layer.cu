@@ -231,7 +231,8 @@ __device__ __noinline__ void fl_topk(const uint32_t* keys, const float* row, int
 // 16 bytes (or, with on = false, zeros) to this lane's place of a ring slot.
 // The L2 is asked for 256 bytes of a row at a time, the next column block with this
 // one: the streams of all warps lie in tens of thousands of rows, and half as many
-// visits to each take 8 tokens from 67.2 to 64.4 us.
+// visits to each took 8 tokens from 67.2 to 64.4 us (before the second term of the
+// hidden values).
 __device__ __forceinline__ void fl_copy16(unsigned char* dst, const void* src, bool on) {
   asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
                "r"(on ? 16u : 0u)
