@@ -80,6 +80,14 @@ def test_small_and_special_blocks():
     same(*quant(x), x.float())
 
 
+def test_large_blocks():
+    x = torch.randn(40, 1024, device="cuda", generator=gen(4)).clamp(-1.9, 1.9)
+    x = x * 2.0 ** torch.arange(88, 128, device="cuda").view(40, 1)      # up to the largest binade
+    x = x.to(torch.bfloat16)
+    assert torch.isfinite(x.float()).all()
+    same(*quant(x), x.float())
+
+
 @pytest.mark.parametrize("d", [256, 2048])
 def test_codes_of_the_norm(d):
     """Rows of +-1 have a mean square of exactly 1, so that with eps = 3, and the
