@@ -529,13 +529,13 @@ __global__ void __launch_bounds__(FG_THREADS, 1) fp8_gemm_kernel(
 // 128 x 256 tiles for many rows.  A k-block takes about 1,130 cycles (8192 x 4096 x
 // 2048: 7 waves of 16 in 77 us at 1.64 GHz under a profiler), of which its MMAs are 540
 // and its 48 KB would be 720 at the 68 bytes per cycle and SM that the L2 was measured
-// to deliver: neither bounds it.  What is left is the round trip of the two accumulators
-// (commit, promotion, hand-back), whose parts were not timed one by one.  Measured in graphs: 8192 x 4096 x 2048 73 us, 20,480
-// rows in 512 groups of 1024 x 2048 204 us, 81,920 rows 300 us; in a long run, under
-// the power cap, the first takes 87 and the last 364 us.  Pairs of SMs on 256 x 256
-// tiles load 32 KB per SM and k-block, but the hand-overs between two SMs cost what
-// that saves (65 against 67 us for the first, 420 against 305 us for the last, on one
-// box).
+// to deliver: neither bounds it.  What is left is the round trip of the two
+// accumulators (commit, promotion, hand-back), whose parts were not timed one by one.
+// Measured in graphs: 8192 x 4096 x 2048 73 us, 20,480 rows in 512 groups of 1024 x 2048
+// 204 us, 81,920 rows 300 us; in a long run, under the power cap, the first takes 87
+// and the last 364 us.  Pairs of SMs on 256 x 256 tiles load 32 KB per SM and k-block,
+// but the hand-overs between two SMs cost what that saves (65 against 67 us for the
+// first, 420 against 305 us for the last, on one box).
 //
 // One tcgen05.mma takes all 256 columns: at 128 columns a block's MMAs read A
 // twice and shared memory at 122 bytes per cycle, which nearly halves their rate.
@@ -889,7 +889,7 @@ GemmPlan plan_fp8_gemm(int M, int N, int G, bool grouped, int sms) {
   // row tiles: the groups hold M rows in all, each at most one partial tile
   const int groups = grouped ? (G < M ? G : M) : 1;
   const long long mt = grouped ? M / FG_BM + groups : (M + FG_BM - 1) / FG_BM;
-  const long long avg = groups ? (M + groups - 1) / groups : 0;
+  const long long avg = groups ? ((long long)M + groups - 1) / groups : 0;
   const long long rows = avg >= FG_BM ? FG_BM : (avg + 31) / 32 * 32;
   const bool few = M <= 32;        // no tile has more than 32 rows
   GemmPlan p = {};

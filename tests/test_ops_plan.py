@@ -49,6 +49,15 @@ def test_no_other_kernel_is_planned(lib):
             assert plan(lib, M, n, 65536) in ALL
 
 
+@pytest.mark.parametrize("groups", [300, 512, 1024])
+@pytest.mark.parametrize("n", [1, 40, 1000, 4096])
+def test_the_most_rows_are_planned_as_a_few_less(lib, groups, n):
+    """Rows and groups add up beyond 2^31 without harm."""
+    want = plan(lib, 2**31 - 4096, n, 16, groups, 1)
+    for M in (2**31 - 1000, 2**31 - 513, 2**31 - 256):
+        assert plan(lib, M, n, 16, groups, 1) == want
+
+
 def test_ring_of_the_wide_kernel(lib):
     """Four stages up to 240 groups."""
     for g, stages in ((1, 4), (240, 4), (241, 3), (1024, 3)):
