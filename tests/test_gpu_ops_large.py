@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from routed_expert_ffn_06_b200 import build, moe, moe_ops
-from _ops_ref import gen, nb
+from _ops_ref import Layer64, gen, nb
 
 pytestmark = pytest.mark.gpu
 FP8 = torch.float8_e4m3fn
@@ -134,3 +134,70 @@ def test_experts(T):
         return y, ids + lo, w
     for a, b in zip(run(0), run(E - k)):
         assert torch.equal(a, b) and torch.isfinite(a.float()).all()
+
+
+MOST = 2**31 - 256        # rows of one call
+
+
+def test_most_rows_of_norm_and_quantiser():
+    """8 channels and the most rows: the first, middle and last ones as alone."""
+    d = 8
+    x = torch.empty(MOST, d, device="cuda", dtype=torch.bfloat16)
+    x.view(-1, 256 * d)[:] = rows(256, d, 21).flatten()
+    x[-1024:] = rows(1024, d, 22)
+    h = torch.empty_like(x)
+    c = torch.empty(MOST, d, device="cuda", dtype=torch.uint8)
+    s = torch.empty(MOST, 1, device="cuda")
+    norm = moe_ops.make_norm(d)
+    moe_ops.moe_norm_block(norm, x, None, None, MOST, None, h, c, s)
+    cuts = [slice(0, 512), slice(MOST // 2 - 256, MOST // 2 + 256), slice(MOST - 1024, MOST)]
+    for cut in cuts:
+        xs = x[cut].clone()
+        hs, cs, ss = torch.empty_like(xs), torch.empty_like(c[cut]), torch.empty_like(s[cut])
+        moe_ops.moe_norm_block(norm, xs, None, None, len(xs), None, hs, cs, ss)
+        assert torch.equal(h[cut], hs) and torch.equal(c[cut], cs) and torch.equal(s[cut], ss)
+    c.zero_(), s.zero_()
+    moe_ops.moe_fp8_quant(x, c, s)
+    for cut in cuts:
+        xs = x[cut].clone()
+        cs, ss = torch.empty_like(c[cut]), torch.empty_like(s[cut])
+        moe_ops.moe_fp8_quant(xs, cs, ss)
+        assert torch.equal(c[cut], cs) and torch.equal(s[cut], ss)
+
+
+@pytest.mark.parametrize("groups", [1, 3])
+def test_most_rows_of_a_product(groups):
+    K, N = 16, 8
+    a = torch.empty(MOST, K, device="cuda", dtype=torch.uint8)
+    a.view(-1, 256 * K)[:] = codes((256, K), 23).view(torch.uint8).flatten()
+    a[-1024:] = codes((1024, K), 24).view(torch.uint8)
+    sa = torch.full((MOST, 1), 0.5, device="cuda")
+    sa[-1024:] = torch.rand(1024, 1, device="cuda", generator=gen(25))
+    w = codes((groups, N, K), 26)
+    sw = torch.rand(groups, 1, 1, device="cuda", generator=gen(27))
+    c = torch.full((MOST, N), 7.0, device="cuda", dtype=torch.bfloat16)
+    ends = [0, MOST] if groups == 1 else [5, 1000, MOST - 700, MOST - 3]
+    if groups == 1:
+        moe_ops.moe_fp8_gemm(moe_ops.make_fp8_mat(w[0], sw[0]), a, sa, MOST, c)
+    else:
+        off = torch.tensor(ends, dtype=torch.int32, device="cuda")
+        moe_ops.moe_fp8_gemm_grouped(moe_ops.make_fp8_mat(w, sw), a, sa, MOST, off, c)
+    for g in range(groups):
+        lo, hi = ends[g], ends[g + 1]
+        for cut in (slice(lo, min(lo + 400, hi)), slice(max(lo, hi - 400), hi)):
+            o = torch.empty(cut.stop - cut.start, N, device="cuda", dtype=torch.bfloat16)
+            moe_ops.moe_fp8_gemm(moe_ops.make_fp8_mat(w[g], sw[g]), a[cut].contiguous(),
+                                 sa[cut].contiguous(), len(o), o)
+            assert torch.equal(c[cut], o)
+    assert (c[:ends[0]] == 7).all() and (c[ends[-1]:] == 7).all()
+
+
+def test_widest_layer():
+    """The largest channels, experts' and shared widths, top-k and window at once."""
+    torch.cuda.empty_cache()
+    L = Layer64(4096, 64, 16, 4096, 4096, seed=31)
+    L.bias[:] = torch.where(torch.arange(64, device="cuda") % 3 == 0, 30.0, 0.0)
+    x = rows(32, 4096, 32)
+    y, ids, w, ws = L.run(x)
+    assert moe.moe_workspace_error(ws) == (0, 0)
+    L.check(x, y, ids, w)
